@@ -10,6 +10,8 @@ or PyTorch fallback: importing fails loudly when ``libsr.so`` is missing.
 Entry points mirror the C ABI:
     gdn_replay      one Gated DeltaNet layer from raw q/k/v/g/beta
     mamba2_replay   the Mamba2 per-head-decay variant
+    linrec_replay   the elementwise gated linear recurrence
+    linrec_backward its gradients
     group_replay    whole groups of GDN layers + MLPs from cached anchors
 """
 from __future__ import annotations
@@ -300,6 +302,175 @@ def mamba2_call(args: Mamba2Args, ws, stream=None) -> int:
 
 def default_scale(d_k):
     return 1.0 / math.sqrt(d_k)
+
+
+# ------------------------------------------------------------------ elementwise recurrence and its gradients
+
+
+class LinrecArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("g", _vp), ("cu_seqlens", _vp), ("h0", _vp), ("y", _vp), ("s_out", _vp),
+                ("dtype", _i32), ("g_dtype", _i32), ("n_seqs", _i32), ("total_tokens", _i32),
+                ("max_seqlen", _i32), ("channels", _i32)]
+
+
+class LinrecGradArgs(ctypes.Structure):
+    _fields_ = [("g", _vp), ("y", _vp), ("dy", _vp), ("cu_seqlens", _vp), ("h0", _vp), ("ds", _vp), ("dx", _vp),
+                ("dg", _vp), ("dh0", _vp), ("dtype", _i32), ("g_dtype", _i32), ("n_seqs", _i32),
+                ("total_tokens", _i32), ("max_seqlen", _i32), ("channels", _i32)]
+
+
+_lr_ws = _sig("sr_linrec_replay_workspace", ctypes.c_size_t, ctypes.POINTER(LinrecArgs))
+_lr = _sig("sr_linrec_replay", _i32, ctypes.POINTER(LinrecArgs), _vp, ctypes.c_size_t, _vp)
+_lrb_ws = _sig("sr_linrec_backward_workspace", ctypes.c_size_t, ctypes.POINTER(LinrecGradArgs))
+_lrb = _sig("sr_linrec_backward", _i32, ctypes.POINTER(LinrecGradArgs), _vp, ctypes.c_size_t, _vp)
+
+
+def _want(t, name, dtypes, shape, device):
+    """Checks an optional or required tensor of a call: a contiguous CUDA tensor on `device`."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_device(device, stream, body):
+    """body(raw stream) with `device` current, and, where a stream is given, that stream too: what body allocates
+    then belongs to the stream that uses it."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        with torch.cuda.stream(stream):
+            return body(ctypes.c_void_p(stream.cuda_stream))
+    if torch.cuda.current_device() == device.index:
+        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    with torch.cuda.device(device):
+        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+
+def _workspace_for(query, call, args, ws, device):
+    """The workspace of a call: the caller's, or a new one.  A query of 0 means that the arguments are refused."""
+    need = query(ctypes.byref(args))
+    if need == 0:
+        _check(call(ctypes.byref(args), None, 0, None))
+    if ws is None:
+        return workspace(need, device)
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous CUDA tensor on {device}")
+    return ws
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
+
+
+def _addr(t):
+    """The address of a required tensor.  An empty one has none: an aligned address that no kernel reads stands in."""
+    return t.data_ptr() or 256
+
+
+def _packed(t, name, cu_seqlens):
+    """Common checks of a packed call: (device, n_seqs) of the first tensor and its boundaries."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must have n_seqs + 1 entries")
+    _want(cu_seqlens, "cu_seqlens", (torch.int32,), tuple(cu_seqlens.shape), t.device)
+    return t.device, cu_seqlens.numel() - 1
+
+
+def linrec_replay(x, g, cu_seqlens, *, max_seqlen, h0=None, want_y=True, y=None, s_out=None, ws=None, stream=None):
+    """Elementwise gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t of every packed sequence (see
+    sr_linrec_replay).
+
+    x: [T, D] bf16/fp32; g: [T, D] fp32 (or bf16 beside a bf16 x); cu_seqlens: [N+1] int32; h0: [N, D] fp32 or
+    None; max_seqlen: host int >= every length.  Returns (y or None, s_out [N, D] fp32); s_out may be h0 itself
+    (a decode step in place).  Not recorded by autograd: linrec_backward gives the gradients."""
+    torch = _torch()
+    dev, n = _packed(x, "x", cu_seqlens)
+    if x.dim() != 2:
+        raise ValueError("x must have 2 dims")
+    T, D = x.shape
+    _want(x, "x", (torch.bfloat16, torch.float32), (T, D), dev)
+    _want(g, "g", (torch.bfloat16, torch.float32), (T, D), dev)
+    if h0 is not None:
+        _want(h0, "h0", (torch.float32,), (n, D), dev)
+    if y is not None:
+        _want(y, "y", (x.dtype,), (T, D), dev)
+    if s_out is not None:
+        _want(s_out, "s_out", (torch.float32,), (n, D), dev)
+
+    def body(st):
+        yy = torch.empty_like(x) if y is None and want_y else y
+        s = torch.empty(n, D, dtype=torch.float32, device=dev) if s_out is None else s_out
+        args = LinrecArgs(_addr(x), _addr(g), cu_seqlens.data_ptr(), None if h0 is None else _addr(h0),
+                          None if yy is None else _addr(yy), _addr(s), SR_FP32 if x.dtype == torch.float32 else SR_BF16,
+                          SR_FP32 if g.dtype == torch.float32 else SR_BF16, n, T, max_seqlen, D)
+        w = _workspace_for(_lr_ws, _lr, args, ws, dev)
+        _check(_lr(ctypes.byref(args), w.data_ptr(), _bytes(w), st))
+        return yy, s
+
+    return _on_device(dev, stream, body)
+
+
+def linrec_backward(g, y, dy, cu_seqlens, *, max_seqlen, h0=None, ds=None, dx=None, dg=None, dh0=None, ws=None,
+                    stream=None):
+    """Gradients of linrec_replay (see sr_linrec_backward): from its g, its output y and the gradients dy of y and
+    ds of s_out (None: zero), with the h0 that it started from.  Returns (dx, dg, dh0)."""
+    torch = _torch()
+    dev, n = _packed(y, "y", cu_seqlens)
+    if y.dim() != 2:
+        raise ValueError("y must have 2 dims")
+    T, D = y.shape
+    _want(y, "y", (torch.bfloat16, torch.float32), (T, D), dev)
+    _want(g, "g", (torch.bfloat16, torch.float32), (T, D), dev)
+    _want(dy, "dy", (y.dtype,), (T, D), dev)
+    for name, t in (("h0", h0), ("ds", ds), ("dh0", dh0)):
+        if t is not None:
+            _want(t, name, (torch.float32,), (n, D), dev)
+    if dx is not None:
+        _want(dx, "dx", (y.dtype,), (T, D), dev)
+    if dg is not None:
+        _want(dg, "dg", (g.dtype,), (T, D), dev)
+
+    def body(st):
+        gx = torch.empty_like(y) if dx is None else dx
+        gg = torch.empty_like(g) if dg is None else dg
+        gh = torch.empty(n, D, dtype=torch.float32, device=dev) if dh0 is None else dh0
+        args = LinrecGradArgs(_addr(g), _addr(y), _addr(dy), cu_seqlens.data_ptr(), None if h0 is None else _addr(h0),
+                              None if ds is None else _addr(ds), _addr(gx), _addr(gg), _addr(gh),
+                              SR_FP32 if y.dtype == torch.float32 else SR_BF16,
+                              SR_FP32 if g.dtype == torch.float32 else SR_BF16, n, T, max_seqlen, D)
+        w = _workspace_for(_lrb_ws, _lrb, args, ws, dev)
+        _check(_lrb(ctypes.byref(args), w.data_ptr(), _bytes(w), st))
+        return gx, gg, gh
+
+    return _on_device(dev, stream, body)
+
+
+def linrec_workspace_bytes(args: LinrecArgs) -> int:
+    return int(_lr_ws(ctypes.byref(args)))
+
+
+def linrec_call(args: LinrecArgs, ws, stream=None) -> int:
+    """Raw C call with prepared args (returns the sr_status)."""
+    return int(_lr(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
+                   _stream_handle(stream) if ws is not None else None))
+
+
+def linrec_backward_workspace_bytes(args: LinrecGradArgs) -> int:
+    return int(_lrb_ws(ctypes.byref(args)))
+
+
+def linrec_backward_call(args: LinrecGradArgs, ws, stream=None) -> int:
+    """Raw C call with prepared args (returns the sr_status)."""
+    return int(_lrb(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
+                    _stream_handle(stream) if ws is not None else None))
 
 
 # ------------------------------------------------------------------ test support (include/sr/sr_testing.h)

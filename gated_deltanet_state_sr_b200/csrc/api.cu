@@ -25,9 +25,7 @@ sr_status cuda_error(cudaError_t e, const char *where) {
     return set_error(SR_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-static bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-static sr_status check_workspace(void *ws, size_t bytes, size_t need) {
+sr_status check_workspace(void *ws, size_t bytes, size_t need) {
     if (!ws) return set_error(SR_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
     if (!aligned(ws, kWsAlign)) return set_error(SR_ERR_WORKSPACE, "workspace not 256-byte aligned");
     if (bytes < need)
@@ -35,7 +33,7 @@ static sr_status check_workspace(void *ws, size_t bytes, size_t need) {
     return SR_OK;
 }
 
-static sr_status check_varlen(int n_seqs, int total, int max_len, const int32_t *cu) {
+sr_status check_varlen(int n_seqs, int total, int max_len, const int32_t *cu) {
     if (!cu) return set_error(SR_ERR_INVALID_ARG, "cu_seqlens is NULL");
     if (n_seqs < 0 || total < 0 || max_len < 0)
         return set_error(SR_ERR_INVALID_ARG, "negative n_seqs / total_tokens / max_seqlen");

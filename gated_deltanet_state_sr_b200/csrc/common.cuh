@@ -20,6 +20,11 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 sr_status set_error(sr_status s, const char *fmt, ...);
 sr_status cuda_error(cudaError_t e, const char *where);
 
+// Host-side checks shared by the entry points (api.cu).
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+sr_status check_workspace(void *ws, size_t bytes, size_t need);
+sr_status check_varlen(int n_seqs, int total, int max_len, const int32_t *cu);
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 

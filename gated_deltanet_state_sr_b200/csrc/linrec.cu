@@ -1,0 +1,420 @@
+// Gated linear recurrence, elementwise over channels, and its gradients.
+//
+// Forward, per sequence and channel, from h_0 (or 0):
+//     h_t = a_t h_{t-1} + x_t,   a_t = exp(g_t),   y_t = h_t.
+// Backward, with the gradient dy_t of every y_t and ds of the last state: let
+// p_t = a_t (dy_t + p_{t+1}), p_{L+1} = ds, be what step t hands to the one
+// before it.  Then
+//     dx_t = dy_t + p_{t+1},   dg_t = p_t h_{t-1},   dh_0 = p_1,
+// a recurrence of the same kind that runs from the last token to the first
+// and reads a_t, dy_t and the stored h_{t-1} of one row each.
+//
+// Both are bound by memory: forward moves x, g in and y out, backward g, dy, y
+// in and dx, dg out, each once.
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace sr {
+namespace {
+
+constexpr int kWarps = 8;   // warps per CTA
+constexpr int kSteps = 8;   // consecutive tokens per warp and wave
+constexpr int kMaxCluster = 8;
+
+struct LinrecParams {
+    const void *in;   // forward x, backward dy   [T, D]
+    const void *g;    // [T, D] log decay
+    const void *y_in; // backward: stored h       [T, D]
+    const int32_t *cu;
+    const float *h0;  // [N, D] or null
+    const float *ds;  // backward: [N, D] or null
+    void *out;        // forward y (may be null), backward dx
+    void *dg;         // backward
+    float *last;      // forward s_out (required), backward dh0 (may be null)
+    uint32_t *status;
+    int n_seqs, total, max_len, D, cluster;
+};
+
+// VEC consecutive elements of a row as fp32.
+template <typename T, int VEC> struct Vec;
+template <> struct Vec<float, 1> {
+    using Raw = float;
+    static __device__ __forceinline__ void get(Raw r, float (&f)[1]) { f[0] = r; }
+    static __device__ __forceinline__ Raw make(const float (&f)[1]) { return f[0]; }
+};
+template <> struct Vec<float, 2> {
+    using Raw = float2;
+    static __device__ __forceinline__ void get(Raw r, float (&f)[2]) { f[0] = r.x, f[1] = r.y; }
+    static __device__ __forceinline__ Raw make(const float (&f)[2]) { return make_float2(f[0], f[1]); }
+};
+template <> struct Vec<__nv_bfloat16, 1> {
+    using Raw = __nv_bfloat16;
+    static __device__ __forceinline__ void get(Raw r, float (&f)[1]) { f[0] = __bfloat162float(r); }
+    static __device__ __forceinline__ Raw make(const float (&f)[1]) { return __float2bfloat16_rn(f[0]); }
+};
+template <> struct Vec<__nv_bfloat16, 2> {
+    using Raw = __nv_bfloat162;
+    static __device__ __forceinline__ void get(Raw r, float (&f)[2]) {
+        const float2 v = __bfloat1622float2(r);
+        f[0] = v.x, f[1] = v.y;
+    }
+    static __device__ __forceinline__ Raw make(const float (&f)[2]) { return __floats2bfloat162_rn(f[0], f[1]); }
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ typename Vec<T, VEC>::Raw load_row(const void *base, long long off, long long n,
+                                                              uint32_t *status) {
+    using Raw = typename Vec<T, VEC>::Raw;
+    Raw r{};
+    if (SR_IN_BOUNDS(off, n, status) && SR_IN_BOUNDS(off + VEC - 1, n, status))
+        r = *reinterpret_cast<const Raw *>(static_cast<const T *>(base) + off);
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(void *base, long long off, long long n, uint32_t *status,
+                                          const float (&f)[VEC]) {
+    using Raw = typename Vec<T, VEC>::Raw;
+    if (SR_IN_BOUNDS(off, n, status) && SR_IN_BOUNDS(off + VEC - 1, n, status))
+        *reinterpret_cast<Raw *>(static_cast<T *>(base) + off) = Vec<T, VEC>::make(f);
+}
+template <int VEC>
+__device__ __forceinline__ void load_state(const float *base, long long off, long long n, uint32_t *status,
+                                           float (&f)[VEC]) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) f[c] = base && SR_IN_BOUNDS(off + c, n, status) ? base[off + c] : 0.f;
+}
+
+// One token's step.  Forward: h = a h + x.  Backward: dx = dy + p, p = a dx.
+template <bool BWD>
+__device__ __forceinline__ float step(float a, float b, float h) {
+    return BWD ? a * (b + h) : fmaf(a, h, b);
+}
+
+// expf, not __expf: a state that decays over n tokens carries n roundings of
+// its decay, and the fast form's error (a few 2^-22, of one sign over a range
+// of g) would add up to 1e-4 at a memory of a thousand tokens.
+__device__ __forceinline__ float decay(float g) { return expf(g); }
+
+// Sequences of a few tokens (a decode step is one): a thread walks one
+// sequence of VEC channels.  No exchange between threads.
+template <typename XT, typename GT, int VEC, bool BWD>
+__global__ void __launch_bounds__(128) linrec_short(LinrecParams p) {
+    const int c0 = (blockIdx.x * 128 + threadIdx.x) * VEC;
+    const int seq = blockIdx.y;
+    if (c0 >= p.D) return;
+    int bos, eos;
+    if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;
+    const long long nel = (long long)p.total * p.D, nst = (long long)p.n_seqs * p.D;
+    const long long soff = (long long)seq * p.D + c0;
+    float h[VEC], h0[VEC];
+    load_state<VEC>(BWD ? p.ds : p.h0, soff, nst, p.status, h);
+    if (BWD) load_state<VEC>(p.h0, soff, nst, p.status, h0);
+    const int len = eos - bos;
+#pragma unroll 4
+    for (int i = 0; i < len; ++i) {
+        const int t = BWD ? eos - 1 - i : bos + i;
+        const long long off = (long long)t * p.D + c0;
+        float a[VEC], b[VEC], prev[VEC], o[VEC];
+        Vec<GT, VEC>::get(load_row<GT, VEC>(p.g, off, nel, p.status), a);
+        Vec<XT, VEC>::get(load_row<XT, VEC>(p.in, off, nel, p.status), b);
+        if (BWD) {
+            if (t > bos)
+                Vec<XT, VEC>::get(load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status), prev);
+            else
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) prev[c] = h0[c];
+        }
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            if (BWD) o[c] = b[c] + h[c];
+            h[c] = step<BWD>(decay(a[c]), b[c], h[c]);
+            if (!BWD) o[c] = h[c];
+            if (BWD) prev[c] *= h[c];
+        }
+        if (BWD) store_row<GT, VEC>(p.dg, off, nel, p.status, prev);
+        if (p.out) store_row<XT, VEC>(p.out, off, nel, p.status, o);
+    }
+    if (p.last)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = h[c];
+}
+
+// Long sequences.  A cluster of C CTAs walks one sequence of 32 VEC channels
+// in waves of C * kWarps * kSteps tokens; warp w of CTA r holds kSteps
+// consecutive tokens of the wave in registers, lane l the channels VEC l ...
+// A run of tokens maps the state entering it as h -> A h + B; every warp folds
+// its own (A, B), a CTA folds its warps', and the CTAs' go to every CTA of the
+// cluster through distributed shared memory.  Then each thread folds the maps
+// before its own in token order, so every sum has one fixed order, and walks
+// its tokens from the state it found.  Nothing is read twice, no flag in
+// global memory is waited on, and the next wave's rows are loaded before the
+// exchange, which they hide.
+template <typename XT, typename GT, int VEC, bool BWD>
+__global__ void __launch_bounds__(kWarps * 32, 2) linrec_scan(LinrecParams p) {
+    constexpr int kCols = 32 * VEC;
+    __shared__ float2 warp_map[2][kWarps][kCols];
+    __shared__ float2 cta_map[2][kMaxCluster][kCols];
+    __shared__ int scratch[kLongestFirstMax + 1];
+    const int C = p.cluster, rank = C > 1 ? int(tc::cluster_ctarank()) : 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = longest_first(p.cu, p.n_seqs, blockIdx.y, scratch);
+    int bos, eos;
+    if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;  // the whole cluster alike
+    if (C > 1) tc::cluster_sync();  // every CTA's shared memory exists before the first remote write
+    const int len = eos - bos;
+    const int c0 = (blockIdx.x / C) * kCols + lane * VEC;
+    const bool col = c0 < p.D;  // VEC divides D
+    const long long nel = (long long)p.total * p.D, nst = (long long)p.n_seqs * p.D;
+    const long long soff = (long long)seq * p.D + c0;
+
+    float carry[VEC], h0[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) carry[c] = h0[c] = 0.f;
+    if (col) {
+        load_state<VEC>(BWD ? p.ds : p.h0, soff, nst, p.status, carry);
+        if (BWD) load_state<VEC>(p.h0, soff, nst, p.status, h0);
+    }
+
+    typename Vec<GT, VEC>::Raw rg[kSteps];
+    typename Vec<XT, VEC>::Raw rx[kSteps], ry[kSteps];
+    const int seg = (rank * kWarps + warp) * kSteps;
+    const int wave = C * kWarps * kSteps;
+    // token of step i in walking order; rows are loaded where they exist
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = base + seg + i;
+            if (col && r < len) {
+                const int t = BWD ? eos - 1 - r : bos + r;
+                const long long off = (long long)t * p.D + c0;
+                rg[i] = load_row<GT, VEC>(p.g, off, nel, p.status);
+                rx[i] = load_row<XT, VEC>(p.in, off, nel, p.status);
+                if (BWD && t > bos) ry[i] = load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status);
+            }
+        }
+    };
+    fetch(0);
+    int par = 0;
+    for (int base = 0; base < len; base += wave, par ^= 1) {
+        float a[kSteps][VEC], b[kSteps][VEC], prev[kSteps][VEC];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = base + seg + i;
+            if (col && r < len) {
+                float g[VEC];
+                Vec<GT, VEC>::get(rg[i], g);
+                Vec<XT, VEC>::get(rx[i], b[i]);
+                if (BWD) Vec<XT, VEC>::get(ry[i], prev[i]);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    a[i][c] = decay(g[c]);
+                    if (BWD && r == len - 1) prev[i][c] = h0[c];
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) a[i][c] = 1.f, b[i][c] = 0.f, prev[i][c] = 0.f;
+            }
+        }
+        if (base + wave < len) fetch(base + wave);
+        // this warp's map
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+            float A = 1.f, B = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                A *= a[i][c];
+                B = step<BWD>(a[i][c], b[i][c], B);
+            }
+            warp_map[par][warp][lane * VEC + c] = make_float2(A, B);
+        }
+        __syncthreads();
+        float h[VEC];
+        if (C > 1) {
+            if (threadIdx.x < kCols) {
+                float A = 1.f, B = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 m = warp_map[par][w][threadIdx.x];
+                    A *= m.x;
+                    B = fmaf(m.x, B, m.y);
+                }
+                const uint32_t mine = tc::smem_u32(&cta_map[par][rank][threadIdx.x]);
+                for (int r = 0; r < C; ++r)
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(tc::mapa_shared(mine, r)), "f"(A),
+                                 "f"(B)
+                                 : "memory");
+            }
+            tc::cluster_sync();
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float v = carry[c];
+                h[c] = v;
+                for (int r = 0; r < C; ++r) {
+                    const float2 m = cta_map[par][r][lane * VEC + c];
+                    v = fmaf(m.x, v, m.y);
+                    if (r + 1 == rank) h[c] = v;
+                }
+                carry[c] = v;
+                for (int w = 0; w < warp; ++w) {
+                    const float2 m = warp_map[par][w][lane * VEC + c];
+                    h[c] = fmaf(m.x, h[c], m.y);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float v = carry[c];
+                h[c] = v;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 m = warp_map[par][w][lane * VEC + c];
+                    v = fmaf(m.x, v, m.y);
+                    if (w + 1 == warp) h[c] = v;
+                }
+                carry[c] = v;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = base + seg + i;
+            if (col && r < len) {
+                const int t = BWD ? eos - 1 - r : bos + r;
+                const long long off = (long long)t * p.D + c0;
+                float o[VEC];
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) {
+                    if (BWD) o[c] = b[i][c] + h[c];
+                    h[c] = step<BWD>(a[i][c], b[i][c], h[c]);
+                    if (!BWD) o[c] = h[c];
+                    if (BWD) prev[i][c] *= h[c];
+                }
+                if (BWD) store_row<GT, VEC>(p.dg, off, nel, p.status, prev[i]);
+                if (p.out) store_row<XT, VEC>(p.out, off, nel, p.status, o);
+            }
+        }
+    }
+    if (p.last && col && rank == 0 && warp == 0)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = carry[c];
+}
+
+// A sequence of at most this many tokens is walked by one thread per channel pair.
+constexpr int kShortLen = 8;
+
+template <typename XT, typename GT, int VEC, bool BWD>
+cudaError_t launch(LinrecParams p, cudaStream_t st) {
+    if (p.max_len <= kShortLen) {
+        const int per = 128 * VEC;
+        linrec_short<XT, GT, VEC, BWD><<<dim3((p.D + per - 1) / per, p.n_seqs), 128, 0, st>>>(p);
+        return cudaGetLastError();
+    }
+    const int blocks = (p.D + 32 * VEC - 1) / (32 * VEC);
+    // A sequence's column block is spread over as many CTAs as fill the GPU
+    // (two per SM), while each still has a full wave of tokens.
+    int C = 1;
+    while (C < kMaxCluster && (long long)blocks * p.n_seqs * C < 2 * 148 && C * kWarps * kSteps < p.max_len) C *= 2;
+    p.cluster = C;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks * C, p.n_seqs);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linrec_scan<XT, GT, VEC, BWD>, p);
+}
+
+template <bool BWD>
+cudaError_t dispatch(const LinrecParams &p, int dtype, int g_dtype, cudaStream_t st) {
+    // Two channels per thread where every row's pairs are aligned.
+    auto pairs = [&](const void *q, int type) { return !q || aligned(q, type == SR_BF16 ? 4 : 8); };
+    const bool two = p.D % 2 == 0 && pairs(p.in, dtype) && pairs(p.g, g_dtype) && pairs(p.y_in, dtype) &&
+                     pairs(p.out, dtype) && pairs(p.dg, g_dtype);
+    if (dtype == SR_FP32)
+        return two ? launch<float, float, 2, BWD>(p, st) : launch<float, float, 1, BWD>(p, st);
+    if (g_dtype == SR_FP32)
+        return two ? launch<__nv_bfloat16, float, 2, BWD>(p, st) : launch<__nv_bfloat16, float, 1, BWD>(p, st);
+    return two ? launch<__nv_bfloat16, __nv_bfloat16, 2, BWD>(p, st)
+               : launch<__nv_bfloat16, __nv_bfloat16, 1, BWD>(p, st);
+}
+
+// Bounds that keep a token's and a channel's index, a wave or block past the end included, in an int.
+constexpr int kMaxTokens = 1 << 30, kMaxChannels = 1 << 24;
+
+sr_status check_types(int dtype, int g_dtype, int channels, int total) {
+    if ((dtype != SR_BF16 && dtype != SR_FP32) || (g_dtype != SR_BF16 && g_dtype != SR_FP32))
+        return set_error(SR_ERR_INVALID_ARG, "bad dtype or g_dtype");
+    if (dtype == SR_FP32 && g_dtype != SR_FP32)
+        return set_error(SR_ERR_UNSUPPORTED, "fp32 rows need an fp32 g");
+    if (channels <= 0) return set_error(SR_ERR_INVALID_ARG, "channels must be positive");
+    if (channels > kMaxChannels || total > kMaxTokens)
+        return set_error(SR_ERR_UNSUPPORTED, "channels > 2^24 or total_tokens > 2^30");
+    return SR_OK;
+}
+
+bool element_aligned(const void *p, int type) { return !p || aligned(p, type == SR_BF16 ? 2 : 4); }
+
+sr_status validate(const sr_linrec_args *a) {
+    if (!a) return set_error(SR_ERR_INVALID_ARG, "args is NULL");
+    if (sr_status s = check_varlen(a->n_seqs, a->total_tokens, a->max_seqlen, a->cu_seqlens)) return s;
+    if (!a->x || !a->g || !a->s_out) return set_error(SR_ERR_INVALID_ARG, "x, g and s_out are required");
+    if (sr_status s = check_types(a->dtype, a->g_dtype, a->channels, a->total_tokens)) return s;
+    if (!element_aligned(a->x, a->dtype) || !element_aligned(a->y, a->dtype) || !element_aligned(a->g, a->g_dtype) ||
+        !aligned(a->h0, 4) || !aligned(a->s_out, 4))
+        return set_error(SR_ERR_INVALID_ARG, "a tensor is not aligned to its element size");
+    return SR_OK;
+}
+
+sr_status validate(const sr_linrec_grad_args *a) {
+    if (!a) return set_error(SR_ERR_INVALID_ARG, "args is NULL");
+    if (sr_status s = check_varlen(a->n_seqs, a->total_tokens, a->max_seqlen, a->cu_seqlens)) return s;
+    if (!a->g || !a->y || !a->dy || !a->dx || !a->dg)
+        return set_error(SR_ERR_INVALID_ARG, "g, y, dy, dx and dg are required");
+    if (sr_status s = check_types(a->dtype, a->g_dtype, a->channels, a->total_tokens)) return s;
+    if (!element_aligned(a->y, a->dtype) || !element_aligned(a->dy, a->dtype) || !element_aligned(a->dx, a->dtype) ||
+        !element_aligned(a->g, a->g_dtype) || !element_aligned(a->dg, a->g_dtype) || !aligned(a->h0, 4) ||
+        !aligned(a->ds, 4) || !aligned(a->dh0, 4))
+        return set_error(SR_ERR_INVALID_ARG, "a tensor is not aligned to its element size");
+    return SR_OK;
+}
+
+template <bool BWD>
+sr_status run(LinrecParams p, int dtype, int g_dtype, void *ws, size_t ws_bytes, void *stream, const char *name) {
+    if (sr_status s = check_workspace(ws, ws_bytes, kWsHeader)) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    p.status = static_cast<uint32_t *>(ws);
+    cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
+    if (e == cudaSuccess && p.n_seqs > 0) e = dispatch<BWD>(p, dtype, g_dtype, st);
+    return e == cudaSuccess ? SR_OK : cuda_error(e, name);
+}
+
+}  // namespace
+}  // namespace sr
+
+using namespace sr;
+
+extern "C" size_t sr_linrec_replay_workspace(const sr_linrec_args *a) { return validate(a) ? 0 : kWsHeader; }
+
+extern "C" sr_status sr_linrec_replay(const sr_linrec_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (sr_status s = validate(a)) return s;
+    LinrecParams p{};
+    p.in = a->x, p.g = a->g, p.cu = a->cu_seqlens, p.h0 = a->h0, p.out = a->y, p.last = a->s_out;
+    p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen, p.D = a->channels;
+    return run<false>(p, a->dtype, a->g_dtype, ws, ws_bytes, stream, "sr_linrec_replay");
+}
+
+extern "C" size_t sr_linrec_backward_workspace(const sr_linrec_grad_args *a) { return validate(a) ? 0 : kWsHeader; }
+
+extern "C" sr_status sr_linrec_backward(const sr_linrec_grad_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (sr_status s = validate(a)) return s;
+    LinrecParams p{};
+    p.in = a->dy, p.g = a->g, p.y_in = a->y, p.cu = a->cu_seqlens, p.h0 = a->h0, p.ds = a->ds;
+    p.out = a->dx, p.dg = a->dg, p.last = a->dh0;
+    p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen, p.D = a->channels;
+    return run<true>(p, a->dtype, a->g_dtype, ws, ws_bytes, stream, "sr_linrec_backward");
+}

@@ -18,6 +18,8 @@
  *                     layer weights (RMSNorm, in_proj, conv, gates, the
  *                     recurrence, gated norm, out_proj, SwiGLU MLP)
  *   sr_mamba2_replay  the Mamba2 per-head-decay variant
+ *   sr_linrec_replay  the elementwise (diagonal) gated linear recurrence, and
+ *                     sr_linrec_backward its gradients
  *
  * Conventions shared by every call
  * --------------------------------
@@ -190,6 +192,85 @@ typedef struct sr_mamba2_args {
 SR_API size_t sr_mamba2_replay_workspace(const sr_mamba2_args *args);
 SR_API sr_status sr_mamba2_replay(const sr_mamba2_args *args, void *workspace, size_t workspace_bytes,
                            void *stream);
+
+/* ------------------------------------------------------------------------
+ * sr_linrec_replay -- elementwise gated linear recurrence.
+ *
+ * The diagonal member of the family S_t = A_t(S_{t-1}) + B_t (SuffixReplay,
+ * Eq. 2): a vector state of `channels` entries with one decay per entry,
+ *     h_t = exp(g_t) h_{t-1} + x_t,   y_t = h_t,
+ * for every packed sequence, starting from h0 (or 0 when h0 is NULL).
+ *
+ *   x          [total_tokens, channels]   dtype (bf16 or fp32)
+ *   g          [total_tokens, channels]   g_dtype, natural-log decay (<= 0;
+ *                                         -inf forgets everything before)
+ *   h0         [n_seqs, channels]         fp32, may be NULL (zero state)
+ *   y          [total_tokens, channels]   dtype, may be NULL (state only)
+ *   s_out      [n_seqs, channels]         fp32, required: the last h of every
+ *                                         sequence; may equal h0 (in place)
+ * The state and every sum are fp32; y is rounded once.  A sequence of length
+ * one is a decode step; one of length zero copies h0 (or 0) to s_out.
+ * Supported: channels in 1..2^24, total_tokens <= 2^30 (two channels per thread when channels is even
+ * and the rows are aligned to pairs); g_dtype fp32, or bf16 with dtype bf16.
+ * Other outputs must not alias inputs.  Results do not depend on timing: the
+ * same call gives the same bits.  Workspace: 256 bytes (the status word).
+ * ---------------------------------------------------------------------- */
+typedef struct sr_linrec_args {
+    const void *x;
+    const void *g;
+    const int32_t *cu_seqlens;
+    const float *h0;
+    void *y;
+    float *s_out;
+    int32_t dtype, g_dtype;  /* sr_dtype */
+    int32_t n_seqs;
+    int32_t total_tokens;
+    int32_t max_seqlen;
+    int32_t channels;
+} sr_linrec_args;
+
+SR_API size_t sr_linrec_replay_workspace(const sr_linrec_args *args);
+SR_API sr_status sr_linrec_replay(const sr_linrec_args *args, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* ------------------------------------------------------------------------
+ * sr_linrec_backward -- gradients of sr_linrec_replay.
+ *
+ * Given g, the stored outputs y and the gradients dy of y and ds of s_out:
+ *     dx_t = dy_t + exp(g_{t+1}) dx_{t+1}   (the last token: dy_t + ds)
+ *     dg_t = dx_t exp(g_t) h_{t-1},   dh0 = exp(g_1) dx_1,
+ * with h_{t-1} read from y (h0, or 0, before the first token).
+ *
+ *   g          [total_tokens, channels]   g_dtype
+ *   y, dy      [total_tokens, channels]   dtype
+ *   h0         [n_seqs, channels]         fp32, may be NULL (zero state)
+ *   ds         [n_seqs, channels]         fp32, may be NULL (zero)
+ *   dx         [total_tokens, channels]   dtype, required
+ *   dg         [total_tokens, channels]   g_dtype, required
+ *   dh0        [n_seqs, channels]         fp32, may be NULL; may equal ds
+ * A sequence of length zero copies ds (or 0) to dh0.  Types, shapes, aliasing
+ * and workspace as in sr_linrec_replay.
+ * ---------------------------------------------------------------------- */
+typedef struct sr_linrec_grad_args {
+    const void *g;
+    const void *y;
+    const void *dy;
+    const int32_t *cu_seqlens;
+    const float *h0;
+    const float *ds;
+    void *dx;
+    void *dg;
+    float *dh0;
+    int32_t dtype, g_dtype;  /* sr_dtype */
+    int32_t n_seqs;
+    int32_t total_tokens;
+    int32_t max_seqlen;
+    int32_t channels;
+} sr_linrec_grad_args;
+
+SR_API size_t sr_linrec_backward_workspace(const sr_linrec_grad_args *args);
+SR_API sr_status sr_linrec_backward(const sr_linrec_grad_args *args, void *workspace, size_t workspace_bytes,
+                                    void *stream);
 
 /* ------------------------------------------------------------------------
  * sr_group_replay -- replay whole linear-attention groups from anchors.

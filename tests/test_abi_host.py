@@ -239,3 +239,67 @@ def test_group_fp8_low_pass_needs_its_weights_and_shapes():
     assert sr.group_workspace_bytes(a) > 0
     a.hidden = 192  # a multiple of 64 but not of 128
     assert sr.group_call(a, None) == sr.SR_ERR_UNSUPPORTED
+
+
+def _linrec(**kw):
+    a = sr.LinrecArgs(x=FAKE, g=FAKE, cu_seqlens=FAKE, h0=FAKE, y=FAKE, s_out=FAKE, dtype=sr.SR_BF16,
+                      g_dtype=sr.SR_FP32, n_seqs=2, total_tokens=100, max_seqlen=60, channels=64)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _linrec_grad(**kw):
+    a = sr.LinrecGradArgs(g=FAKE, y=FAKE, dy=FAKE, cu_seqlens=FAKE, h0=FAKE, ds=FAKE, dx=FAKE, dg=FAKE, dh0=FAKE,
+                          dtype=sr.SR_BF16, g_dtype=sr.SR_BF16, n_seqs=2, total_tokens=100, max_seqlen=60,
+                          channels=64)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+_LINREC_BAD = [
+    ("g", None, sr.SR_ERR_INVALID_ARG),
+    ("cu_seqlens", None, sr.SR_ERR_INVALID_ARG),
+    ("channels", 0, sr.SR_ERR_INVALID_ARG),
+    ("channels", (1 << 24) + 1, sr.SR_ERR_UNSUPPORTED),
+    ("n_seqs", -1, sr.SR_ERR_INVALID_ARG),
+    ("n_seqs", 65536, sr.SR_ERR_UNSUPPORTED),
+    ("total_tokens", (1 << 30) + 1, sr.SR_ERR_UNSUPPORTED),
+    ("max_seqlen", 101, sr.SR_ERR_INVALID_ARG),
+    ("dtype", 5, sr.SR_ERR_INVALID_ARG),
+    ("g_dtype", -1, sr.SR_ERR_INVALID_ARG),
+    ("y", FAKE + 1, sr.SR_ERR_INVALID_ARG),
+    ("g", FAKE + 1, sr.SR_ERR_INVALID_ARG),
+    ("h0", FAKE + 2, sr.SR_ERR_INVALID_ARG),
+]
+
+
+@pytest.mark.parametrize("field,value,status", _LINREC_BAD + [("x", None, sr.SR_ERR_INVALID_ARG),
+                                                              ("s_out", None, sr.SR_ERR_INVALID_ARG)])
+def test_linrec_validation(field, value, status):
+    a = _linrec(**{field: value})
+    assert sr.linrec_workspace_bytes(a) == 0
+    assert sr.linrec_call(a, None) == status
+    assert sr.last_error() != ""
+
+
+@pytest.mark.parametrize("field,value,status", _LINREC_BAD + [("dy", None, sr.SR_ERR_INVALID_ARG),
+                                                              ("dx", None, sr.SR_ERR_INVALID_ARG),
+                                                              ("dg", FAKE + 1, sr.SR_ERR_INVALID_ARG),
+                                                              ("ds", FAKE + 2, sr.SR_ERR_INVALID_ARG)])
+def test_linrec_backward_validation(field, value, status):
+    a = _linrec_grad(**{field: value})
+    assert sr.linrec_backward_workspace_bytes(a) == 0
+    assert sr.linrec_backward_call(a, None) == status
+    assert sr.last_error() != ""
+
+
+def test_linrec_workspace_is_checked_before_any_launch():
+    a = _linrec(h0=None, y=None)
+    assert sr.linrec_workspace_bytes(a) == 256
+    assert sr.linrec_call(a, None) == sr.SR_ERR_WORKSPACE
+    b = _linrec_grad(h0=None, ds=None, dh0=None)
+    assert sr.linrec_backward_workspace_bytes(b) == 256
+    assert sr.linrec_backward_call(b, None) == sr.SR_ERR_WORKSPACE
+    assert sr.linrec_call(_linrec(dtype=sr.SR_FP32, g_dtype=sr.SR_BF16), None) == sr.SR_ERR_UNSUPPORTED
