@@ -12,6 +12,7 @@ Entry points mirror the C ABI:
     mamba2_replay   the Mamba2 per-head-decay variant
     linrec_replay   the elementwise gated linear recurrence
     linrec_backward its gradients
+    kv_append       rotated keys and values into a paged 8-bit cache
     group_replay    whole groups of GDN layers + MLPs from cached anchors
 """
 from __future__ import annotations
@@ -41,6 +42,7 @@ SR_BF16, SR_FP32 = 0, 1
 SR_GDN_AUTO, SR_GDN_SEQUENTIAL, SR_GDN_CHUNKED, SR_GDN_TCGEN05, SR_GDN_TCGEN05_FUSED = 0, 1, 2, 3, 4
 SR_MODE_SKIP, SR_MODE_FULL = 0, 1
 SR_DEV_BAD_CU_SEQLENS, SR_DEV_SEQ_TOO_LONG, SR_DEV_TIMEOUT, SR_DEV_BAD_INDEX, SR_DEV_BAD_ACCESS = 0x1, 0x2, 0x4, 0x8, 0x10
+SR_DEV_BAD_LENGTH = 0x20
 CHECKED = _LIB_NAME == "libsr_checked.so"
 _ALGOS = {"auto": SR_GDN_AUTO, "sequential": SR_GDN_SEQUENTIAL, "chunked": SR_GDN_CHUNKED,
           "tcgen05": SR_GDN_TCGEN05, "tcgen05_fused": SR_GDN_TCGEN05_FUSED}
@@ -470,6 +472,114 @@ def linrec_backward_workspace_bytes(args: LinrecGradArgs) -> int:
 def linrec_backward_call(args: LinrecGradArgs, ws, stream=None) -> int:
     """Raw C call with prepared args (returns the sr_status)."""
     return int(_lrb(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
+                    _stream_handle(stream) if ws is not None else None))
+
+
+# ------------------------------------------------------------------ paged 8-bit key/value cache
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [(f, _vp) for f in ("k", "v", "q", "q_out", "positions", "inv_freq", "cu_seqlens", "kv_lens",
+                                   "block_table", "k_cache", "v_cache", "k_scale", "v_scale")] + [
+        (f, ctypes.c_int64) for f in ("k_stride", "v_stride", "q_stride", "q_out_stride")] + [
+        (f, _i32) for f in ("n_seqs", "total_tokens", "max_seqlen", "h_q", "h_kv", "head_dim", "page_size", "n_pages",
+                            "max_pages", "rot_dim", "interleaved", "n_axes")] + [("sections", _i32 * 3)]
+
+
+_kva_ws = _sig("sr_kv_append_workspace", ctypes.c_size_t, ctypes.POINTER(KvAppendArgs))
+_kva = _sig("sr_kv_append", _i32, ctypes.POINTER(KvAppendArgs), _vp, ctypes.c_size_t, _vp)
+
+
+def _rows(t, name, heads, d, tokens, device):
+    """Checks a [T, heads, d] bf16 tensor whose tokens may lie further apart than their heads fill (a slice of a fused
+    projection) and returns the distance in elements."""
+    torch = _torch()
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must have shape {(tokens, heads, d)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != d):
+        raise ValueError(f"{name}: a token's heads must lie together")
+    return s[0] if tokens > 1 else heads * d
+
+
+def _cache(cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, device, n):
+    torch = _torch()
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must have 4 dims, block_table 2")
+    pages, h_kv, page, d = k_cache.shape
+    _want(kv_lens, "kv_lens", (torch.int32,), (n,), device)
+    _want(block_table, "block_table", (torch.int32,), (n, block_table.shape[1]), device)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _want(t, name, (torch.float8_e4m3fn, torch.uint8), (pages, h_kv, page, d), device)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _want(t, name, (torch.float32,), (pages, h_kv), device)
+    return pages, h_kv, page, d
+
+
+def kv_append(k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, max_seqlen, q=None,
+              q_out=None, inv_freq=None, positions=None, sections=None, interleaved=False, ws=None, stream=None):
+    """Appends the new tokens' keys and values to a paged 8-bit cache, rotating keys and queries (see sr_kv_append).
+
+    k, v: [T, H_kv, d] bf16; q: [T, H_q, d] bf16 or None (tokens may be strided); cu_seqlens: [N+1] int32;
+    kv_lens: [N] int32, tokens cached once the new ones are in; block_table: [N, P] int32; k_cache, v_cache:
+    [pages, H_kv, page_size, d] float8_e4m3fn (or its bytes as uint8); k_scale, v_scale: [pages, H_kv] fp32;
+    inv_freq: [rot_dim / 2] fp32, or None for no rotation; positions: [T] or [axes, T] int32, or None for the cache
+    positions; sections: pairs of each axis (default: all of one axis).  max_seqlen bounds a sequence's new tokens.
+    The caches and scales are updated in place.  Returns the rotated queries (q_out, or a new tensor), or None
+    without q."""
+    torch = _torch()
+    dev, n = _packed(k, "k", cu_seqlens)
+    pages, h_kv, page, d = _cache(cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, dev, n)
+    T = k.shape[0]
+    ks, vs = _rows(k, "k", h_kv, d, T, dev), _rows(v, "v", h_kv, d, T, dev)
+    h_q = qs = os_ = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must have 3 dims")
+        h_q = q.shape[1]
+        qs = _rows(q, "q", h_q, d, T, dev)
+        if q_out is not None:
+            os_ = _rows(q_out, "q_out", h_q, d, T, dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    half = 0
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        _want(inv_freq, "inv_freq", (torch.float32,), (half,), dev)
+    axes = 1
+    if positions is not None:
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        _want(positions, "positions", (torch.int32,), (axes, T) if positions.dim() == 2 else (T,), dev)
+    sections = [half] if sections is None else [int(s) for s in sections]
+    if len(sections) != axes or axes > 3:
+        raise ValueError(f"sections must have one entry for each of the {axes} axes (at most 3)")
+
+    def body(st):
+        out = torch.empty(T, h_q, d, dtype=torch.bfloat16, device=dev) if q is not None and q_out is None else q_out
+        a = KvAppendArgs(_addr(k), _addr(v), None if q is None else _addr(q), None if out is None else _addr(out),
+                         None if positions is None else _addr(positions), None if inv_freq is None else _addr(inv_freq),
+                         cu_seqlens.data_ptr(), _addr(kv_lens), _addr(block_table), _addr(k_cache), _addr(v_cache),
+                         _addr(k_scale), _addr(v_scale), ks, vs, qs, os_ if q_out is not None else h_q * d, n, T,
+                         max_seqlen, h_q, h_kv, d, page, pages, block_table.shape[1], 2 * half, int(interleaved), axes,
+                         (_i32 * 3)(*sections))
+        w = _workspace_for(_kva_ws, _kva, a, ws, dev)
+        _check(_kva(ctypes.byref(a), w.data_ptr(), _bytes(w), st))
+        return out
+
+    return _on_device(dev, stream, body)
+
+
+def kv_append_workspace_bytes(args: KvAppendArgs) -> int:
+    return int(_kva_ws(ctypes.byref(args)))
+
+
+def kv_append_call(args: KvAppendArgs, ws, stream=None) -> int:
+    """Raw C call with prepared args (returns the sr_status)."""
+    return int(_kva(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
                     _stream_handle(stream) if ws is not None else None))
 
 

@@ -24,6 +24,7 @@ sr_status cuda_error(cudaError_t e, const char *where);
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 sr_status check_workspace(void *ws, size_t bytes, size_t need);
 sr_status check_varlen(int n_seqs, int total, int max_len, const int32_t *cu);
+sr_status check_cache(int n_pages, int max_pages, int page, int h_q, int h_kv, int d, bool queries);  // kv_append.cu
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

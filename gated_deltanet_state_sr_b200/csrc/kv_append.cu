@@ -1,0 +1,305 @@
+// Appending keys and values to a paged 8-bit cache, with the position rotation
+// of queries and keys on the way.
+//
+// Per token, head and rotated pair i, with the angle f = position * inv_freq[i]
+// of the axis that pair i belongs to: (lo, hi) -> (lo cos f - hi sin f,
+// lo sin f + hi cos f).  A page of a head is a block with one power-of-two
+// scale s; a value x is stored as e4m3(x / s), so storing and reading back cost
+// one rounding and no other.  Where new tokens join older ones in a page, the
+// page keeps the larger of its scale and what the new ones need, and the older
+// bytes are rounded again if it grew (dividing by a power of two is exact, so
+// only values that fall into e4m3's least binade change).
+//
+// Bound by memory: queries 2 + 2 bytes a value, keys and values 2 + 1.  One
+// CTA per page of a sequence's new tokens (and per share of the heads): it
+// forms the page's cosines and sines once, in shared memory, for all its heads,
+// since an angle (64-bit product, reduced to a fraction of a turn, because a
+// position of 10^6 times 1 rad leaves fp32 no fraction) costs more than the
+// rotation itself.  A warp takes one head of the page: keys and values in two
+// passes over the bf16 rows, the first for the largest magnitude, the second
+// from the caches that the first filled.
+#include "paged.cuh"
+
+namespace sr {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr double kTurnsPerRadian = 0.15915494309189533577;  // 1 / (2 pi)
+
+struct AppendParams {
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16 *q_out;
+    const int32_t *positions;  // [axes, T] or null
+    const float *inv_freq;     // [rot / 2]
+    const int32_t *cu, *kv_lens, *table;
+    uint8_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    uint32_t *status;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    int n_seqs, total, max_len, h_q, h_kv, page, n_pages, max_pages, half, interleaved, sec0, sec1, groups;
+};
+
+// Eight elements of a token's head that one lane holds: four rotated pairs
+// (4u .. 4u+3) for u < half / 4, eight elements without rotation beyond.
+struct Unit {
+    int lo, hi;   // element offsets of the two 4-element parts
+    int pair;     // first pair, or -1
+};
+
+template <int D>
+__device__ __forceinline__ Unit unit_of(int u, int half, int interleaved) {
+    Unit r;
+    if (u < half / 4) {
+        r.pair = 4 * u;
+        r.lo = interleaved ? 8 * u : 4 * u;
+        r.hi = interleaved ? 8 * u + 4 : half + 4 * u;
+    } else {
+        r.pair = -1;
+        r.lo = 8 * u;
+        r.hi = 8 * u + 4;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void unpack(uint2 r, float *f) {
+    f[0] = __uint_as_float(r.x << 16);
+    f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16);
+    f[3] = __uint_as_float(r.y & 0xffff0000u);
+}
+
+// f[0..3] at u.lo, f[4..7] at u.hi.
+__device__ __forceinline__ void rotate(float (&f)[8], const Unit &u, const float2 *cs, int interleaved) {
+    if (u.pair < 0) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 c = cs[u.pair + j];
+        float &lo = interleaved ? f[2 * j] : f[j], &hi = interleaved ? f[2 * j + 1] : f[4 + j];
+        const float a = lo, b = hi;
+        lo = a * c.x - b * c.y;
+        hi = a * c.y + b * c.x;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
+    constexpr int kLanes = D / 8;         // lanes per token
+    constexpr int kAtOnce = 32 / kLanes;  // tokens per warp and step
+    extern __shared__ float2 table_cs[];  // [tokens of the page][half]
+    const int seq = blockIdx.z;
+    int bos, eos;
+    if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;
+    if (bos == eos) return;
+    const int kv = p.kv_lens[seq], start = kv - (eos - bos);
+    if (start < 0 || kv > (long long)p.max_pages * p.page) {
+        if (threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_LENGTH);
+        return;
+    }
+    const int slot = start / p.page + blockIdx.x;  // page of the sequence
+    const int from = max(start, slot * p.page), to = min(kv, (slot + 1) * p.page);
+    if (from >= to) return;
+    const int n = to - from, tok0 = bos + (from - start);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    for (int i = threadIdx.x; i < n * p.half; i += kWarps * 32) {
+        const int t = i / p.half, pair = i - t * p.half;
+        const int axis = (pair >= p.sec0) + (pair >= p.sec1);
+        const long long at = (long long)axis * p.total + tok0 + t;
+        const int pos = !p.positions ? from + t : SR_IN_BOUNDS(at, 3ll * p.total, p.status) ? p.positions[at] : 0;
+        const double turns = double(pos) * double(p.inv_freq[pair]) * kTurnsPerRadian;
+        float s, c;
+        sincospif(2.f * float(turns - rint(turns)), &s, &c);
+        table_cs[i] = make_float2(c, s);
+    }
+    __syncthreads();
+
+    const int page = p.table[(long long)seq * p.max_pages + slot];
+    const bool page_ok = page >= 0 && page < p.n_pages;
+    if (!page_ok && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
+    const Unit u = unit_of<D>(lane % kLanes, p.half, p.interleaved);
+    const Unit plain{8 * (lane % kLanes), 8 * (lane % kLanes) + 4, -1};
+    const int sub = lane / kLanes;
+    const int heads = p.h_q + 2 * p.h_kv;
+    for (int item = blockIdx.y * kWarps + warp; item < heads; item += p.groups * kWarps) {
+        if (item >= 2 * p.h_kv) {  // a query head: rotated rows
+            if (!p.q) break;
+            const int h = item - 2 * p.h_kv;
+            const __nv_bfloat16 *src = p.q + (long long)tok0 * p.q_stride + h * D;
+            __nv_bfloat16 *dst = p.q_out + (long long)tok0 * p.q_out_stride + h * D;
+#pragma unroll 4
+            for (int t = sub; t < n; t += kAtOnce) {
+                float f[8];
+                const __nv_bfloat16 *row = src + t * p.q_stride;
+                unpack(*reinterpret_cast<const uint2 *>(row + u.lo), f);
+                unpack(*reinterpret_cast<const uint2 *>(row + u.hi), f + 4);
+                rotate(f, u, table_cs + t * p.half, p.interleaved);
+                __nv_bfloat16 *out = dst + t * p.q_out_stride;
+                *reinterpret_cast<uint2 *>(out + u.lo) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+                *reinterpret_cast<uint2 *>(out + u.hi) = make_uint2(pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+            }
+            continue;
+        }
+        if (!page_ok) continue;
+        const bool key = item < p.h_kv;
+        const int h = key ? item : item - p.h_kv;
+        const Unit w = key ? u : plain;
+        const long long stride = key ? p.k_stride : p.v_stride;
+        const __nv_bfloat16 *src = (key ? p.k : p.v) + (long long)tok0 * stride + h * D;
+        const long long block = (long long)page * p.h_kv + h;
+        uint8_t *cache = (key ? p.k_cache : p.v_cache) + block * p.page * D;
+        float *scale = (key ? p.k_scale : p.v_scale) + block;
+        auto value = [&](int t, float (&f)[8]) {
+            const __nv_bfloat16 *row = src + t * stride;
+            unpack(*reinterpret_cast<const uint2 *>(row + w.lo), f);
+            unpack(*reinterpret_cast<const uint2 *>(row + w.hi), f + 4);
+            rotate(f, w, table_cs + t * p.half, p.interleaved);
+        };
+        float top = 0.f;
+#pragma unroll 4
+        for (int t = sub; t < n; t += kAtOnce) {
+            float f[8];
+            value(t, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float m = fabsf(f[j]);
+                if (m <= 3.402823466e38f) top = fmaxf(top, m);  // a value that is not finite has no part in the scale
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int old = from - slot * p.page;  // tokens that the page held before
+        const float before = old > 0 ? *scale : 0.f;
+        const float kept = fmaxf(before, ldexpf(1.f, paged::scale_exp(top)));
+        __syncwarp();  // every lane has read the old scale
+        if (lane == 0) *scale = kept;
+        if (old > 0 && before != kept) {
+            const float ratio = before / kept;
+            for (int t = sub; t < old; t += kAtOnce) {
+                uint2 *at = reinterpret_cast<uint2 *>(cache + t * D + plain.lo);
+                uint2 r = *at;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t &x = j ? r.y : r.x;
+                    const float2 a = paged::e4m3x2_to_float2(x), b = paged::e4m3x2_to_float2(x >> 16);
+                    x = paged::to_e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+                }
+                *at = r;
+            }
+        }
+        const float inv = 1.f / kept;
+#pragma unroll 4
+        for (int t = sub; t < n; t += kAtOnce) {
+            float f[8];
+            value(t, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= inv;
+            uint8_t *out = cache + (old + t) * D;
+            *reinterpret_cast<uint32_t *>(out + w.lo) = paged::to_e4m3x4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint32_t *>(out + w.hi) = paged::to_e4m3x4(f[4], f[5], f[6], f[7]);
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch(AppendParams p, cudaStream_t st) {
+    const int slots = (p.max_len + p.page - 2) / p.page + 1;  // pages that max_len tokens can touch
+    const int heads = (p.q ? p.h_q : 0) + 2 * p.h_kv;
+    // The heads of a page are shared out over as many CTAs as give the GPU eight warps per scheduler; every share
+    // repeats the page's cosines and sines, so no more than that.
+    const long long tiles = (long long)slots * p.n_seqs;
+    const int most = (heads + kWarps - 1) / kWarps;
+    const long long want = (4 * 148 + tiles - 1) / tiles;
+    p.groups = int(want < most ? want : most);
+    const size_t smem = size_t(p.page < p.max_len ? p.page : p.max_len) * p.half * sizeof(float2);
+    static_assert(128 * 128 * sizeof(float2) <= 227 * 1024, "the largest table fits");
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(append_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    append_kernel<D><<<dim3(slots, p.groups, p.n_seqs), kWarps * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+sr_status validate(const sr_kv_append_args *a) {
+    if (!a) return set_error(SR_ERR_INVALID_ARG, "args is NULL");
+    if (sr_status s = check_varlen(a->n_seqs, a->total_tokens, a->max_seqlen, a->cu_seqlens)) return s;
+    if (a->total_tokens > (1 << 30)) return set_error(SR_ERR_UNSUPPORTED, "total_tokens > 2^30");
+    if (sr_status s = check_cache(a->n_pages, a->max_pages, a->page_size, a->h_q, a->h_kv, a->head_dim, a->q != nullptr))
+        return s;
+    if (!a->k || !a->v || !a->kv_lens || !a->block_table || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)
+        return set_error(SR_ERR_INVALID_ARG, "k, v, kv_lens, block_table, caches and scales are required");
+    if (!a->q != !a->q_out) return set_error(SR_ERR_INVALID_ARG, "q and q_out come together");
+    if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 8)
+        return set_error(SR_ERR_UNSUPPORTED, "rot_dim must be a multiple of 8 in 0..head_dim (got %d)", a->rot_dim);
+    if (a->rot_dim > 0 && !a->inv_freq) return set_error(SR_ERR_INVALID_ARG, "inv_freq is required with rot_dim > 0");
+    if (a->n_axes < 1 || a->n_axes > 3) return set_error(SR_ERR_UNSUPPORTED, "n_axes must be 1, 2 or 3");
+    int sum = 0;
+    for (int i = 0; i < a->n_axes; ++i) {
+        if (a->sections[i] < 0 || a->sections[i] > a->rot_dim)
+            return set_error(SR_ERR_INVALID_ARG, "sections[%d] is out of range", i);
+        sum += a->sections[i];
+    }
+    if (sum != a->rot_dim / 2) return set_error(SR_ERR_INVALID_ARG, "sections must add up to rot_dim / 2");
+    if (a->n_axes > 1 && !a->positions) return set_error(SR_ERR_INVALID_ARG, "several axes need positions");
+    const struct { const void *p; int64_t stride; int heads; const char *name; } rows[] = {
+        {a->k, a->k_stride, a->h_kv, "k"}, {a->v, a->v_stride, a->h_kv, "v"},
+        {a->q, a->q_stride, a->h_q, "q"}, {a->q_out, a->q_out_stride, a->h_q, "q_out"}};
+    for (const auto &r : rows)
+        if (r.p && (r.stride < int64_t(r.heads) * a->head_dim || r.stride % 8 || !aligned(r.p, 16)))
+            return set_error(SR_ERR_INVALID_ARG, "%s: 16-byte aligned, its token stride a multiple of 8 and no less than "
+                             "a token's heads", r.name);
+    if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->k_scale, 4) || !aligned(a->v_scale, 4))
+        return set_error(SR_ERR_INVALID_ARG, "caches must be 16-byte aligned, scales 4-byte");
+    return SR_OK;
+}
+
+}  // namespace
+
+sr_status check_cache(int n_pages, int max_pages, int page, int h_q, int h_kv, int d, bool queries) {
+    if (n_pages < 0 || max_pages < 0) return set_error(SR_ERR_INVALID_ARG, "negative n_pages or max_pages");
+    if (page != 16 && page != 32 && page != 64 && page != 128)
+        return set_error(SR_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128 (got %d)", page);
+    if (d != 64 && d != 128 && d != 256)
+        return set_error(SR_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", d);
+    if (h_kv <= 0 || (queries && (h_q <= 0 || h_q % h_kv)))
+        return set_error(SR_ERR_INVALID_ARG, "need h_kv > 0 and h_q a multiple of it (h_q=%d h_kv=%d)", h_q, h_kv);
+    if (h_kv > 1024 || h_q > 4096) return set_error(SR_ERR_UNSUPPORTED, "h_kv > 1024 or h_q > 4096");
+    if ((long long)max_pages * page > (1 << 30))
+        return set_error(SR_ERR_UNSUPPORTED, "max_pages * page_size > 2^30");
+    return SR_OK;
+}
+
+}  // namespace sr
+
+using namespace sr;
+
+extern "C" size_t sr_kv_append_workspace(const sr_kv_append_args *a) { return validate(a) ? 0 : kWsHeader; }
+
+extern "C" sr_status sr_kv_append(const sr_kv_append_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (sr_status s = validate(a)) return s;
+    if (sr_status s = check_workspace(ws, ws_bytes, kWsHeader)) return s;
+    AppendParams p{};
+    p.k = static_cast<const __nv_bfloat16 *>(a->k), p.v = static_cast<const __nv_bfloat16 *>(a->v);
+    p.q = static_cast<const __nv_bfloat16 *>(a->q), p.q_out = static_cast<__nv_bfloat16 *>(a->q_out);
+    p.positions = a->positions, p.inv_freq = a->inv_freq;
+    p.cu = a->cu_seqlens, p.kv_lens = a->kv_lens, p.table = a->block_table;
+    p.k_cache = static_cast<uint8_t *>(a->k_cache), p.v_cache = static_cast<uint8_t *>(a->v_cache);
+    p.k_scale = a->k_scale, p.v_scale = a->v_scale;
+    p.status = static_cast<uint32_t *>(ws);
+    p.k_stride = a->k_stride, p.v_stride = a->v_stride, p.q_stride = a->q_stride, p.q_out_stride = a->q_out_stride;
+    p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen;
+    p.h_q = a->q ? a->h_q : 0, p.h_kv = a->h_kv, p.page = a->page_size, p.n_pages = a->n_pages;
+    p.max_pages = a->max_pages, p.half = a->rot_dim / 2, p.interleaved = a->interleaved != 0;
+    p.sec0 = a->n_axes > 1 ? a->sections[0] : p.half;
+    p.sec1 = a->n_axes > 2 ? a->sections[0] + a->sections[1] : p.half;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
+    if (e == cudaSuccess && p.n_seqs > 0 && p.max_len > 0)
+        e = a->head_dim == 64 ? launch<64>(p, st) : a->head_dim == 128 ? launch<128>(p, st) : launch<256>(p, st);
+    return e == cudaSuccess ? SR_OK : cuda_error(e, "sr_kv_append");
+}

@@ -20,6 +20,8 @@
  *   sr_mamba2_replay  the Mamba2 per-head-decay variant
  *   sr_linrec_replay  the elementwise (diagonal) gated linear recurrence, and
  *                     sr_linrec_backward its gradients
+ *   sr_kv_append      the full-attention layers between groups: new keys and
+ *                     values into a paged 8-bit cache, rotated on the way
  *
  * Conventions shared by every call
  * --------------------------------
@@ -82,6 +84,7 @@ typedef enum sr_dtype { SR_BF16 = 0, SR_FP32 = 1 } sr_dtype;
 #define SR_DEV_BAD_INDEX 0x8u       /* an anchor or row index outside its table (row read as zero / skipped) */
 #define SR_DEV_BAD_ACCESS 0x10u     /* bounds-checked build (libsr_checked.so) only: a global-memory access
                                        outside its buffer was found and skipped */
+#define SR_DEV_BAD_LENGTH 0x20u     /* a kv_lens entry out of range (its sequence is skipped) */
 
 /* Kernel selection for sr_gdn_replay. */
 typedef enum sr_gdn_algo {
@@ -503,6 +506,74 @@ typedef struct sr_capture_args {
 
 SR_API sr_status sr_anchor_capture(const sr_capture_args *args, void *workspace, size_t workspace_bytes,
                                    void *stream);
+
+/* ------------------------------------------------------------------------
+ * sr_kv_append -- new keys and values into a paged 8-bit cache, rotated.
+ *
+ * The full-attention layers between two replay groups keep an exact cache of
+ * keys and values in pages, beside which the anchors lie ("SuffixReplay",
+ * System Design, Anchor Sidecar).  For every sequence n, its new tokens are
+ * the rows cu_seqlens[n]..cu_seqlens[n+1] of k and v; kv_lens[n] tokens are in
+ * the cache once they are appended, so the i-th goes to position
+ * kv_lens[n] - new + i, which lies in page block_table[n][position /
+ * page_size].  In the same pass keys, and queries where q is given, are rotated:
+ * pair i of the first rot_dim elements by the angle positions[axis][token] *
+ * inv_freq[i], where the first sections[0] pairs take axis 0, the next
+ * sections[1] axis 1, and so on (time, height and width of a picture's
+ * tokens; text has one axis).  Pair i is elements (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) with interleaved != 0; the elements behind rot_dim stay.
+ *
+ *   k, v       [total_tokens, h_kv, head_dim] bf16, a token's heads together,
+ *              tokens k_stride / v_stride elements apart (a multiple of 8)
+ *   q, q_out   [total_tokens, h_q, head_dim] bf16, likewise; both NULL for
+ *              keys and values alone; q_out may be q
+ *   positions  [n_axes, total_tokens] int32, or NULL: the cache position
+ *   inv_freq   [rot_dim / 2] fp32
+ *   kv_lens    [n_seqs] int32, the new tokens included
+ *   block_table  [n_seqs, max_pages] int32
+ *   k_cache, v_cache  [n_pages, h_kv, page_size, head_dim] e4m3 bytes
+ *   k_scale, v_scale  [n_pages, h_kv] fp32: a byte b stands for b * scale
+ * Stored values.  Rotation is in fp32 (angles in 64 bits), and a value is
+ * rounded once, to e4m3.  The scale of a page's head is the least power of two
+ * s in 2^-32..2^32 with max|x| <= 449 s over its tokens; a page that held
+ * tokens before keeps the larger of its old scale and what the new tokens
+ * need, and where it grew the old bytes are rounded to the new one.  A page
+ * whose first token this call writes starts afresh, whatever it held.  Values
+ * that are not finite are stored as NaN and have no part in the scale.
+ * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; rot_dim a
+ * multiple of 8 in 0..head_dim; n_axes 1..3.  No two sequences may write to
+ * the same page in one call.  A page number outside [0, n_pages) leaves its
+ * tokens out and sets SR_DEV_BAD_INDEX; a kv_lens entry below the number of new
+ * tokens or above max_pages * page_size skips the sequence and sets
+ * SR_DEV_BAD_LENGTH.  Workspace: 256 bytes (the status word).
+ * ---------------------------------------------------------------------- */
+typedef struct sr_kv_append_args {
+    const void *k;
+    const void *v;
+    const void *q;
+    void *q_out;
+    const int32_t *positions;
+    const float *inv_freq;
+    const int32_t *cu_seqlens;
+    const int32_t *kv_lens;
+    const int32_t *block_table;
+    void *k_cache;
+    void *v_cache;
+    float *k_scale;
+    float *v_scale;
+    int64_t k_stride, v_stride, q_stride, q_out_stride; /* elements from token to token */
+    int32_t n_seqs;
+    int32_t total_tokens;
+    int32_t max_seqlen;   /* bound of the new tokens of a sequence */
+    int32_t h_q, h_kv, head_dim;
+    int32_t page_size, n_pages, max_pages;
+    int32_t rot_dim, interleaved;
+    int32_t n_axes;
+    int32_t sections[3];
+} sr_kv_append_args;
+
+SR_API size_t sr_kv_append_workspace(const sr_kv_append_args *args);
+SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * sr_sparse_anchor_plan -- host: which anchors a token-sparse replay reads.

@@ -303,3 +303,53 @@ def test_linrec_workspace_is_checked_before_any_launch():
     assert sr.linrec_backward_workspace_bytes(b) == 256
     assert sr.linrec_backward_call(b, None) == sr.SR_ERR_WORKSPACE
     assert sr.linrec_call(_linrec(dtype=sr.SR_FP32, g_dtype=sr.SR_BF16), None) == sr.SR_ERR_UNSUPPORTED
+
+
+def _kv_append(**kw):
+    a = sr.KvAppendArgs(k=FAKE, v=FAKE, q=FAKE, q_out=FAKE, positions=FAKE, inv_freq=FAKE, cu_seqlens=FAKE,
+                        kv_lens=FAKE, block_table=FAKE, k_cache=FAKE, v_cache=FAKE, k_scale=FAKE, v_scale=FAKE,
+                        k_stride=256, v_stride=256, q_stride=512, q_out_stride=512, n_seqs=2, total_tokens=100,
+                        max_seqlen=60, h_q=4, h_kv=2, head_dim=128, page_size=64, n_pages=9, max_pages=4, rot_dim=64,
+                        interleaved=0, n_axes=3)
+    a.sections[0], a.sections[1], a.sections[2] = 16, 8, 8
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("field,value,status", [
+    ("k", None, sr.SR_ERR_INVALID_ARG),
+    ("kv_lens", None, sr.SR_ERR_INVALID_ARG),
+    ("block_table", None, sr.SR_ERR_INVALID_ARG),
+    ("v_scale", None, sr.SR_ERR_INVALID_ARG),
+    ("q_out", None, sr.SR_ERR_INVALID_ARG),      # q without q_out
+    ("inv_freq", None, sr.SR_ERR_INVALID_ARG),
+    ("positions", None, sr.SR_ERR_INVALID_ARG),  # three axes need positions
+    ("k_stride", 248, sr.SR_ERR_INVALID_ARG),    # less than a token's heads
+    ("q_stride", 516, sr.SR_ERR_INVALID_ARG),    # not a multiple of 8
+    ("v", FAKE + 8, sr.SR_ERR_INVALID_ARG),
+    ("k_cache", FAKE + 8, sr.SR_ERR_INVALID_ARG),
+    ("h_q", 5, sr.SR_ERR_INVALID_ARG),
+    ("h_kv", 0, sr.SR_ERR_INVALID_ARG),
+    ("head_dim", 96, sr.SR_ERR_UNSUPPORTED),
+    ("page_size", 48, sr.SR_ERR_UNSUPPORTED),
+    ("rot_dim", 60, sr.SR_ERR_UNSUPPORTED),
+    ("rot_dim", 136, sr.SR_ERR_UNSUPPORTED),
+    ("rot_dim", 128, sr.SR_ERR_INVALID_ARG),     # sections add up to 32
+    ("n_axes", 2, sr.SR_ERR_INVALID_ARG),        # 16 + 8
+    ("n_axes", 4, sr.SR_ERR_UNSUPPORTED),
+    ("max_pages", -1, sr.SR_ERR_INVALID_ARG),
+    ("max_seqlen", 101, sr.SR_ERR_INVALID_ARG),
+    ("total_tokens", (1 << 30) + 1, sr.SR_ERR_UNSUPPORTED),
+])
+def test_kv_append_validation(field, value, status):
+    a = _kv_append(**{field: value})
+    assert sr.kv_append_workspace_bytes(a) == 0
+    assert sr.kv_append_call(a, None) == status
+    assert sr.last_error() != ""
+
+
+def test_kv_append_workspace():
+    assert sr.kv_append_workspace_bytes(_kv_append()) == 256
+    assert sr.kv_append_call(_kv_append(), None) == sr.SR_ERR_WORKSPACE
+    assert sr.kv_append_workspace_bytes(_kv_append(q=None, q_out=None, h_q=0)) == 256
