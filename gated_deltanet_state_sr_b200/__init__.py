@@ -13,6 +13,7 @@ Entry points mirror the C ABI:
     linrec_replay   the elementwise gated linear recurrence
     linrec_backward its gradients
     kv_append       rotated keys and values into a paged 8-bit cache
+    paged_attention attention over that cache
     group_replay    whole groups of GDN layers + MLPs from cached anchors
 """
 from __future__ import annotations
@@ -580,6 +581,60 @@ def kv_append_workspace_bytes(args: KvAppendArgs) -> int:
 def kv_append_call(args: KvAppendArgs, ws, stream=None) -> int:
     """Raw C call with prepared args (returns the sr_status)."""
     return int(_kva(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
+                    _stream_handle(stream) if ws is not None else None))
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [(f, _vp) for f in ("q", "cu_seqlens", "kv_lens", "block_table", "k_cache", "v_cache", "k_scale",
+                                   "v_scale", "o", "lse")] + [("q_stride", ctypes.c_int64)] + [
+        (f, _i32) for f in ("n_seqs", "total_tokens", "max_seqlen", "max_kvlen", "h_q", "h_kv", "head_dim",
+                            "page_size", "n_pages", "max_pages")] + [("scale", ctypes.c_float)]
+
+
+_att_ws = _sig("sr_paged_attention_workspace", ctypes.c_size_t, ctypes.POINTER(PagedAttentionArgs))
+_att = _sig("sr_paged_attention", _i32, ctypes.POINTER(PagedAttentionArgs), _vp, ctypes.c_size_t, _vp)
+
+
+def paged_attention(q, cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, max_seqlen, max_kvlen,
+                    o=None, lse=None, want_lse=False, scale=0.0, ws=None, stream=None):
+    """Causal attention of every sequence's new tokens over its paged 8-bit cache (see sr_paged_attention).
+
+    q: [T, H_q, d] bf16 (tokens may be strided), the rows cu_seqlens[n]..cu_seqlens[n+1] being the last tokens of
+    sequence n's kv_lens[n] cached ones; cache tensors as in kv_append; max_seqlen and max_kvlen: host ints that bound
+    the new and the cached tokens of a sequence.  Returns (o [T, H_q, d] bf16, lse [T, H_q] fp32 or None)."""
+    torch = _torch()
+    dev, n = _packed(q, "q", cu_seqlens)
+    pages, h_kv, page, d = _cache(cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, dev, n)
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dims")
+    T, h_q = q.shape[0], q.shape[1]
+    qs = _rows(q, "q", h_q, d, T, dev)
+    if o is not None:
+        _want(o, "o", (torch.bfloat16,), (T, h_q, d), dev)
+    if lse is not None:
+        _want(lse, "lse", (torch.float32,), (T, h_q), dev)
+
+    def body(st):
+        out = torch.empty(T, h_q, d, dtype=torch.bfloat16, device=dev) if o is None else o
+        ll = torch.empty(T, h_q, dtype=torch.float32, device=dev) if lse is None and want_lse else lse
+        a = PagedAttentionArgs(_addr(q), cu_seqlens.data_ptr(), _addr(kv_lens), _addr(block_table), _addr(k_cache),
+                               _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(out),
+                               None if ll is None else _addr(ll), qs, n, T, max_seqlen, max_kvlen, h_q, h_kv, d, page,
+                               pages, block_table.shape[1], float(scale))
+        w = _workspace_for(_att_ws, _att, a, ws, dev)
+        _check(_att(ctypes.byref(a), w.data_ptr(), _bytes(w), st))
+        return out, ll
+
+    return _on_device(dev, stream, body)
+
+
+def paged_attention_workspace_bytes(args: PagedAttentionArgs) -> int:
+    return int(_att_ws(ctypes.byref(args)))
+
+
+def paged_attention_call(args: PagedAttentionArgs, ws, stream=None) -> int:
+    """Raw C call with prepared args (returns the sr_status)."""
+    return int(_att(ctypes.byref(args), _ptr(ws), 0 if ws is None else _bytes(ws),
                     _stream_handle(stream) if ws is not None else None))
 
 

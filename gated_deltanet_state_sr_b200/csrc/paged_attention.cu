@@ -1,0 +1,80 @@
+// Host side of attention over the paged 8-bit cache: checks, workspace, maps.
+#include <math.h>
+
+#include "paged_attention.cuh"
+#include "kernels.h"
+
+namespace sr {
+namespace paged {
+namespace {
+
+// Tickets, then the partial sums: two parts of 16 rows for every CTA.
+size_t tickets_bytes() { return align_up(kRowsMaxCtas * sizeof(int), kWsAlign); }
+constexpr size_t kPartSlots = 2 * kRowsMaxCtas;
+size_t parts_bytes(int d) {
+    return kPartSlots * 16 * (size_t(d) * sizeof(float) + sizeof(float2));
+}
+size_t need(const sr_paged_attention_args *a) { return kWsHeader + tickets_bytes() + parts_bytes(a->head_dim); }
+
+sr_status validate(const sr_paged_attention_args *a) {
+    if (!a) return set_error(SR_ERR_INVALID_ARG, "args is NULL");
+    if (sr_status s = check_varlen(a->n_seqs, a->total_tokens, a->max_seqlen, a->cu_seqlens)) return s;
+    if (sr_status s = check_cache(a->n_pages, a->max_pages, a->page_size, a->h_q, a->h_kv, a->head_dim, true)) return s;
+    if (!a->q || !a->o || !a->kv_lens || !a->block_table || !a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale)
+        return set_error(SR_ERR_INVALID_ARG, "q, o, kv_lens, block_table, caches and scales are required");
+    if (a->max_kvlen < 0 || a->max_kvlen > (1 << 30))
+        return set_error(SR_ERR_INVALID_ARG, "max_kvlen must be in 0..2^30");
+    if (a->h_q / a->h_kv > 64) return set_error(SR_ERR_UNSUPPORTED, "h_q / h_kv > 64");
+    if ((long long)a->total_tokens * (a->h_q / a->h_kv) > (1 << 30))
+        return set_error(SR_ERR_UNSUPPORTED, "total_tokens * h_q / h_kv > 2^30");
+    if ((long long)a->n_pages * a->h_kv * a->page_size > INT32_MAX)
+        return set_error(SR_ERR_UNSUPPORTED, "n_pages * h_kv * page_size > 2^31 - 1");
+    if (a->q_stride < int64_t(a->h_q) * a->head_dim || a->q_stride % 8 || !aligned(a->q, 16))
+        return set_error(SR_ERR_INVALID_ARG,
+                         "q: 16-byte aligned, its token stride a multiple of 8 and no less than a token's heads");
+    if (!aligned(a->o, 16) || !aligned(a->lse, 4) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16))
+        return set_error(SR_ERR_INVALID_ARG, "o and the caches must be 16-byte aligned, lse 4-byte");
+    if (!isfinite(a->scale)) return set_error(SR_ERR_INVALID_ARG, "scale is not finite");
+    return SR_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace sr
+
+using namespace sr;
+
+extern "C" size_t sr_paged_attention_workspace(const sr_paged_attention_args *a) {
+    return paged::validate(a) ? 0 : paged::need(a);
+}
+
+extern "C" sr_status sr_paged_attention(const sr_paged_attention_args *a, void *ws, size_t ws_bytes, void *stream) {
+    if (sr_status s = paged::validate(a)) return s;
+    if (sr_status s = check_workspace(ws, ws_bytes, paged::need(a))) return s;
+    paged::AttnParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(a->q), p.q_stride = a->q_stride;
+    p.cu = a->cu_seqlens, p.kv_lens = a->kv_lens, p.table = a->block_table;
+    p.k_scale = a->k_scale, p.v_scale = a->v_scale;
+    p.o = static_cast<__nv_bfloat16 *>(a->o), p.lse = a->lse;
+    char *w = static_cast<char *>(ws);
+    p.status = reinterpret_cast<uint32_t *>(w);
+    p.tickets = reinterpret_cast<int *>(w + kWsHeader);
+    p.parts = reinterpret_cast<float *>(w + kWsHeader + paged::tickets_bytes());
+    p.part_ml = reinterpret_cast<float2 *>(p.parts + paged::kPartSlots * 16 * a->head_dim);
+    p.scale_log2 = (a->scale != 0.f ? a->scale : 1.f / sqrtf(float(a->head_dim))) * 1.44269504088896341f;
+    p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen, p.max_kv = a->max_kvlen;
+    p.h_q = a->h_q, p.h_kv = a->h_kv, p.group = a->h_q / a->h_kv;
+    p.page = a->page_size, p.n_pages = a->n_pages, p.max_pages = a->max_pages;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader + paged::tickets_bytes(), st);
+    if (e != cudaSuccess) return cuda_error(e, "sr_paged_attention: clearing the status word");
+    if (p.n_seqs == 0 || p.total == 0) return SR_OK;
+    // boxes of a page's rows (64 at most) and 128 columns (64 at head dimension 64)
+    const int rows = a->n_pages * a->h_kv * a->page_size, box = a->page_size < 64 ? a->page_size : 64;
+    CUtensorMap km, vm;
+    if (rows == 0) return set_error(SR_ERR_INVALID_ARG, "the cache has no pages");
+    if (!make_map_cache(&km, a->k_cache, rows, a->head_dim, box) || !make_map_cache(&vm, a->v_cache, rows, a->head_dim, box))
+        return set_error(SR_ERR_CUDA, "sr_paged_attention: encoding the tensor maps");
+    e = paged::attend_rows(km, vm, p, a->head_dim, st);
+    return e == cudaSuccess ? SR_OK : cuda_error(e, "sr_paged_attention");
+}

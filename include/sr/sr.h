@@ -22,6 +22,7 @@
  *                     sr_linrec_backward its gradients
  *   sr_kv_append      the full-attention layers between groups: new keys and
  *                     values into a paged 8-bit cache, rotated on the way
+ *   sr_paged_attention  and the attention of the new tokens over that cache
  *
  * Conventions shared by every call
  * --------------------------------
@@ -574,6 +575,64 @@ typedef struct sr_kv_append_args {
 
 SR_API size_t sr_kv_append_workspace(const sr_kv_append_args *args);
 SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * sr_paged_attention -- attention over the paged 8-bit cache.
+ *
+ * The unmatched tokens behind a cached prefix (or a request's next token) meet
+ * the cached keys and values of a full-attention layer: for the i-th of
+ * sequence n's new = cu_seqlens[n+1] - cu_seqlens[n] rows and query head h,
+ * whose keys and values are head h / (h_q / h_kv)'s,
+ *     o = sum_t softmax_t(scale q . k_t) v_t,   t < kv_lens[n] - new + i + 1
+ * over the cached tokens in block_table order: causal, the new tokens being
+ * the last ones of the cache (sr_kv_append with the same kv_lens put them
+ * there).  A row that sees no token (kv_lens[n] < new) has o = 0 and lse = -inf.
+ *
+ *   q          [total_tokens, h_q, head_dim] bf16, a token's heads together,
+ *              tokens q_stride elements apart (a multiple of 8)
+ *   kv_lens, block_table, k_cache, v_cache, k_scale, v_scale  as in
+ *              sr_kv_append; a scale outside 2^-32..2^32 is taken as the nearer
+ *              bound
+ *   o          [total_tokens, h_q, head_dim] bf16
+ *   lse        [total_tokens, h_q] fp32, may be NULL: log sum_t exp(scale q . k_t)
+ *   scale      0 selects 1/sqrt(head_dim)
+ * Scores, softmax statistics and sums are fp32; the weights and queries meet
+ * the tensor cores in half precision (eleven bits), keys and values exactly.
+ * Tokens that a row does not see have no part in it, whatever they hold (NaN
+ * bytes included).  The same call gives the same bits.
+ * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; h_q / h_kv
+ * up to 64; n_pages * h_kv * page_size < 2^31.  max_seqlen bounds a sequence's
+ * new tokens, max_kvlen its cached ones.  A page number outside [0, n_pages)
+ * among a sequence's ceil(kv_lens[n] / page_size) skips the sequence and sets
+ * SR_DEV_BAD_INDEX; a kv_lens entry below 0, above max_kvlen or above max_pages *
+ * page_size skips it and sets SR_DEV_BAD_LENGTH.  Workspace: what
+ * sr_paged_attention_workspace returns (about 5 MB: partial sums of sequences
+ * whose cache several CTAs share); calls that overlap need one each.
+ * ---------------------------------------------------------------------- */
+typedef struct sr_paged_attention_args {
+    const void *q;
+    const int32_t *cu_seqlens;
+    const int32_t *kv_lens;
+    const int32_t *block_table;
+    const void *k_cache;
+    const void *v_cache;
+    const float *k_scale;
+    const float *v_scale;
+    void *o;
+    float *lse;
+    int64_t q_stride; /* elements from token to token */
+    int32_t n_seqs;
+    int32_t total_tokens;
+    int32_t max_seqlen;
+    int32_t max_kvlen;
+    int32_t h_q, h_kv, head_dim;
+    int32_t page_size, n_pages, max_pages;
+    float scale;
+} sr_paged_attention_args;
+
+SR_API size_t sr_paged_attention_workspace(const sr_paged_attention_args *args);
+SR_API sr_status sr_paged_attention(const sr_paged_attention_args *args, void *workspace, size_t workspace_bytes,
+                                    void *stream);
 
 /* ------------------------------------------------------------------------
  * sr_sparse_anchor_plan -- host: which anchors a token-sparse replay reads.

@@ -353,3 +353,46 @@ def test_kv_append_workspace():
     assert sr.kv_append_workspace_bytes(_kv_append()) == 256
     assert sr.kv_append_call(_kv_append(), None) == sr.SR_ERR_WORKSPACE
     assert sr.kv_append_workspace_bytes(_kv_append(q=None, q_out=None, h_q=0)) == 256
+
+
+def _paged_attention(**kw):
+    a = sr.PagedAttentionArgs(q=FAKE, cu_seqlens=FAKE, kv_lens=FAKE, block_table=FAKE, k_cache=FAKE, v_cache=FAKE,
+                              k_scale=FAKE, v_scale=FAKE, o=FAKE, lse=FAKE, q_stride=1024, n_seqs=2, total_tokens=100,
+                              max_seqlen=60, max_kvlen=500, h_q=8, h_kv=2, head_dim=128, page_size=64, n_pages=9,
+                              max_pages=8, scale=0.0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("field,value,status", [
+    ("q", None, sr.SR_ERR_INVALID_ARG),
+    ("o", None, sr.SR_ERR_INVALID_ARG),
+    ("kv_lens", None, sr.SR_ERR_INVALID_ARG),
+    ("k_scale", None, sr.SR_ERR_INVALID_ARG),
+    ("cu_seqlens", None, sr.SR_ERR_INVALID_ARG),
+    ("q", FAKE + 8, sr.SR_ERR_INVALID_ARG),
+    ("lse", FAKE + 2, sr.SR_ERR_INVALID_ARG),
+    ("q_stride", 1016, sr.SR_ERR_INVALID_ARG),
+    ("q_stride", 1028, sr.SR_ERR_INVALID_ARG),
+    ("h_q", 9, sr.SR_ERR_INVALID_ARG),
+    ("h_q", 130, sr.SR_ERR_UNSUPPORTED),        # 65 heads to one
+    ("head_dim", 192, sr.SR_ERR_UNSUPPORTED),
+    ("page_size", 8, sr.SR_ERR_UNSUPPORTED),
+    ("max_kvlen", -1, sr.SR_ERR_INVALID_ARG),
+    ("max_pages", 1 << 28, sr.SR_ERR_UNSUPPORTED),
+    ("n_pages", 1 << 25, sr.SR_ERR_UNSUPPORTED),  # 2^32 rows of the cache
+    ("total_tokens", 1 << 30, sr.SR_ERR_UNSUPPORTED),
+    ("max_seqlen", 101, sr.SR_ERR_INVALID_ARG),
+    ("scale", float("inf"), sr.SR_ERR_INVALID_ARG),
+])
+def test_paged_attention_validation(field, value, status):
+    a = _paged_attention(**{field: value})
+    assert sr.paged_attention_workspace_bytes(a) == 0
+    assert sr.paged_attention_call(a, None) == status
+    assert sr.last_error() != ""
+
+
+def test_paged_attention_workspace():
+    assert sr.paged_attention_workspace_bytes(_paged_attention()) % 8 == 0
+    assert sr.paged_attention_call(_paged_attention(), None) == sr.SR_ERR_WORKSPACE
