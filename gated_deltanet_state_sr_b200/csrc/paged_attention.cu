@@ -8,13 +8,18 @@ namespace sr {
 namespace paged {
 namespace {
 
-// Tickets, then the partial sums: two parts of 16 rows for every CTA.
-size_t tickets_bytes() { return align_up(kRowsMaxCtas * sizeof(int), kWsAlign); }
-constexpr size_t kPartSlots = 2 * kRowsMaxCtas;
-size_t parts_bytes(int d) {
-    return kPartSlots * 16 * (size_t(d) * sizeof(float) + sizeof(float2));
+// Few rows: what one mma tile holds.
+bool few_rows(const sr_paged_attention_args *a) { return (long long)a->max_seqlen * (a->h_q / a->h_kv) <= 16; }
+
+// Tickets, then the partial sums (two parts for every CTA) and their statistics.
+constexpr size_t kTickets = 2 * (kRowsMaxCtas > kPromptCtas ? kRowsMaxCtas : kPromptCtas);
+size_t tickets_bytes() { return align_up(kTickets * sizeof(int), kWsAlign); }
+size_t part_rows(const sr_paged_attention_args *a) {
+    return few_rows(a) ? 2 * kRowsMaxCtas * 16 : size_t(2 * kPromptCtas) * prompt_rows(a->head_dim);
 }
-size_t need(const sr_paged_attention_args *a) { return kWsHeader + tickets_bytes() + parts_bytes(a->head_dim); }
+size_t need(const sr_paged_attention_args *a) {
+    return kWsHeader + tickets_bytes() + part_rows(a) * (size_t(a->head_dim) * sizeof(float) + sizeof(float2));
+}
 
 sr_status validate(const sr_paged_attention_args *a) {
     if (!a) return set_error(SR_ERR_INVALID_ARG, "args is NULL");
@@ -60,7 +65,8 @@ extern "C" sr_status sr_paged_attention(const sr_paged_attention_args *a, void *
     p.status = reinterpret_cast<uint32_t *>(w);
     p.tickets = reinterpret_cast<int *>(w + kWsHeader);
     p.parts = reinterpret_cast<float *>(w + kWsHeader + paged::tickets_bytes());
-    p.part_ml = reinterpret_cast<float2 *>(p.parts + paged::kPartSlots * 16 * a->head_dim);
+    p.part_ml = reinterpret_cast<float2 *>(p.parts + paged::part_rows(a) * a->head_dim);
+    p.v_cache = static_cast<const uint8_t *>(a->v_cache);
     p.scale_log2 = (a->scale != 0.f ? a->scale : 1.f / sqrtf(float(a->head_dim))) * 1.44269504088896341f;
     p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen, p.max_kv = a->max_kvlen;
     p.h_q = a->h_q, p.h_kv = a->h_kv, p.group = a->h_q / a->h_kv;
@@ -75,6 +81,7 @@ extern "C" sr_status sr_paged_attention(const sr_paged_attention_args *a, void *
     if (rows == 0) return set_error(SR_ERR_INVALID_ARG, "the cache has no pages");
     if (!make_map_cache(&km, a->k_cache, rows, a->head_dim, box) || !make_map_cache(&vm, a->v_cache, rows, a->head_dim, box))
         return set_error(SR_ERR_CUDA, "sr_paged_attention: encoding the tensor maps");
-    e = paged::attend_rows(km, vm, p, a->head_dim, st);
+    e = paged::few_rows(a) ? paged::attend_rows(km, vm, p, a->head_dim, st)
+                           : paged::attend_prompt(km, vm, p, a->head_dim, st);
     return e == cudaSuccess ? SR_OK : cuda_error(e, "sr_paged_attention");
 }

@@ -103,66 +103,10 @@ template <int D> struct RowsSmem {
         float row_scale[16];       // factor of q . k of each row
         int row_seen[16];          // tokens each row may see
         float sums[16];
-        long long scan[kThreads / 32];
-        long long total, base;
-        int seq, ticket;
+        LinePlace place;
+        int ticket;
     };
     static constexpr int bytes = off_misc + int(sizeof(Misc)) + 1024;  // + alignment of the stages
-};
-
-// The walk of one CTA along its part of the line of blocks.
-struct Segment {
-    int seq, head, tile, rows;       // rows: of this tile
-    int b0, b1;                      // blocks, clipped to what the tile's rows see
-    int bos, count, kv;              // the sequence: first row, new tokens, cached tokens
-    int first_cta, last_cta;         // CTAs that hold the unit's blocks
-};
-
-struct Line {
-    const AttnParams *p;
-    long long cur, end, base, cost, total;
-    int seq, ctas, blocks, tiles, bos, count, kv;
-
-    // Blocks of sequence n in the line; 0 where its entries are out of range.
-    __device__ long long load(int n, bool flag) {
-        int b = p->cu[n], e = p->cu[n + 1], k = p->kv_lens[n];
-        uint32_t bad = 0;
-        if (b < 0 || b > e || e > p->total || (n == 0 && b != 0)) bad = SR_DEV_BAD_CU_SEQLENS;
-        else if (e - b > p->max_len) bad = SR_DEV_SEQ_TOO_LONG;
-        else if (k < 0 || k > p->max_kv || k > (long long)p->max_pages * p->page) bad = SR_DEV_BAD_LENGTH;
-        if (bad) {
-            if (flag) atomicOr(p->status, bad);
-            e = b;
-        }
-        bos = b, count = e - b, kv = bad ? 0 : k;
-        tiles = (count * p->group + 15) / 16;
-        blocks = (kv + kTok - 1) / kTok;
-        if (blocks == 0) blocks = 1;  // rows that see nothing are still written
-        return (long long)tiles * blocks * p->h_kv;
-    }
-
-    __device__ bool next(Segment &s) {
-        if (cur >= end) return false;
-        while (cur >= base + cost) {
-            base += cost;
-            cost = load(++seq, false);
-        }
-        const long long local = cur - base;
-        const int unit = int(local / blocks), b = int(local - (long long)unit * blocks);
-        const int n = int(min((long long)(blocks - b), end - cur));
-        s.seq = seq, s.head = unit / tiles, s.tile = unit - s.head * tiles;
-        s.bos = bos, s.count = count, s.kv = kv;
-        s.rows = min(16, count * p->group - s.tile * 16);
-        const int last_token = (s.tile * 16 + s.rows - 1) / p->group;
-        const int seen = max(0, kv - count + last_token + 1);
-        s.b0 = b;
-        s.b1 = max(b, min(b + n, (seen + kTok - 1) / kTok));
-        const long long first = base + (long long)unit * blocks;
-        s.first_cta = int(((first + 1) * ctas - 1) / total);
-        s.last_cta = int(((first + blocks) * ctas - 1) / total);
-        cur += n;
-        return true;
-    }
 };
 
 template <int D>
@@ -176,58 +120,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     typename S::Misc &misc = *reinterpret_cast<typename S::Misc *>(smem + S::off_misc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // ---- this CTA's part of the line
-    Line line;
-    line.p = &p;
-    {
-        long long mine = 0;
-        for (int n = threadIdx.x; n < p.n_seqs; n += kThreads) mine += line.load(n, blockIdx.x == 0);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) misc.scan[warp] = mine;
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < kStages; ++i) {
-                tc::mbar_init(&misc.full[i], 1);
-                tc::mbar_init(&misc.empty[i], 4);
-            }
-            tc::fence_mbar_init();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&misc.full[i], 1);
+            tc::mbar_init(&misc.empty[i], 4);
         }
-        __syncthreads();
-        long long total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) total += misc.scan[w];
-        if (total == 0) return;
-        line.total = total;
-        line.ctas = int(min((long long)gridDim.x, (total + kMinBlocks - 1) / kMinBlocks));
-        if (int(blockIdx.x) >= line.ctas) return;
-        line.cur = blockIdx.x * total / line.ctas;
-        line.end = (blockIdx.x + 1) * total / line.ctas;
-        // the sequence that holds block `cur`
-        long long before = 0;
-        for (int n0 = 0; n0 < p.n_seqs; n0 += kThreads) {
-            const int n = n0 + threadIdx.x;
-            const long long c = n < p.n_seqs ? line.load(n, false) : 0;
-            long long incl = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
-            }
-            __syncthreads();
-            if (lane == 31) misc.scan[warp] = incl;
-            __syncthreads();
-            long long at = before + incl - c, chunk = 0;
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) at += misc.scan[w];
-                chunk += misc.scan[w];
-            }
-            if (c > 0 && line.cur >= at && line.cur < at + c) misc.seq = n, misc.base = at;
-            before += chunk;
-            if (before > line.cur) break;
-        }
-        __syncthreads();
-        line.seq = misc.seq, line.base = misc.base;
-        line.cost = line.load(line.seq, false);
+        tc::fence_mbar_init();
     }
+    Line<16, kTok> line;
+    if (!line.start<kThreads>(p, kMinBlocks, misc.place)) return;
 
     const uint32_t stage0 = tc::smem_u32(smem);
     Segment seg;

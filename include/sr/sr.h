@@ -596,8 +596,10 @@ SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, si
  *   o          [total_tokens, h_q, head_dim] bf16
  *   lse        [total_tokens, h_q] fp32, may be NULL: log sum_t exp(scale q . k_t)
  *   scale      0 selects 1/sqrt(head_dim)
- * Scores, softmax statistics and sums are fp32; the weights and queries meet
- * the tensor cores in half precision (eleven bits), keys and values exactly.
+ * Scores, softmax statistics and sums are fp32; the weights meet the tensor
+ * cores in half precision (eleven bits), keys and values exactly, queries
+ * exactly down to 2^-9 of their row's largest element and within 2^-17 of that
+ * below.
  * Tokens that a row does not see have no part in it, whatever they hold (NaN
  * bytes included).  The same call gives the same bits.
  * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; h_q / h_kv
@@ -606,8 +608,8 @@ SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, si
  * among a sequence's ceil(kv_lens[n] / page_size) skips the sequence and sets
  * SR_DEV_BAD_INDEX; a kv_lens entry below 0, above max_kvlen or above max_pages *
  * page_size skips it and sets SR_DEV_BAD_LENGTH.  Workspace: what
- * sr_paged_attention_workspace returns (about 5 MB: partial sums of sequences
- * whose cache several CTAs share); calls that overlap need one each.
+ * sr_paged_attention_workspace returns (1 to 39 MB: partial sums of rows whose
+ * cache several CTAs share); calls that overlap need one each.
  * ---------------------------------------------------------------------- */
 typedef struct sr_paged_attention_args {
     const void *q;

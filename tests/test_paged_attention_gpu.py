@@ -2,8 +2,9 @@
 
 Bounds.  A weight meets the tensor cores in half precision: 2^-11 of itself.  A
 score is an fp32 sum of d products (2^-23 of their magnitudes' sum each, in
-whatever order), its query element exact in half precision down to 2^-14 of the
-row's largest and off by 2^-25 of that below; a score's error e moves its
+whatever order), its query element exact down to 2^-9 of the row's largest and
+off by 2^-17 of that below (two e4m3 numbers; half precision, for few rows, is
+closer); a score's error e moves its
 weight by e (1 + e).  With three roundings of fp32 sums and factors beside
 (2^-20 covers them), o is within (2^-11 + 2 e + 2^-20) sum p |v| and a last
 rounding to bf16, 2^-8 of itself; weights under 2^-35 of the largest are lost,
@@ -92,7 +93,7 @@ def check(sr, c, scale=None, **kw):
         for h in range(q.shape[1]):
             g = h // c["group"]
             qa = np.abs(q[rows, h])
-            e[rows, h] = abs(sc) * (c["d"] * 2.0 ** -23 * (qa @ kk[g]) + 2.0 ** -25 * qa.max(-1) * kk[g].sum())
+            e[rows, h] = abs(sc) * (c["d"] * 2.0 ** -23 * (qa @ kk[g]) + 2.0 ** -17 * qa.max(-1) * kk[g].sum())
             v_most[rows, h] = vv[g]
     assert e.max() < 0.05, "the bound says nothing"
     longest = max(c["kv"])
@@ -239,7 +240,7 @@ def test_same_bits_again_captured_and_on_two_streams(sr, new, kv):
     kw = dict(max_seqlen=max(new), max_kvlen=max(kv))
     rest = (c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"])
     o, lse = torch.zeros_like(ref[0]), torch.zeros_like(ref[1])
-    ws = sr.workspace(16 << 20)
+    ws = sr.workspace(64 << 20)
     ws.fill_(255)  # whatever a workspace held before
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
@@ -267,7 +268,7 @@ def test_bad_pages_and_lengths_skip_their_sequence(sr):
     for new in ([1, 1, 1], [40, 3, 200]):
         c = make(new, [400, 90, 300], 4, 2, 128, 64, seed=18)
         ref = call(sr, c)
-        ws = sr.workspace(16 << 20)
+        ws = sr.workspace(64 << 20)
 
         def skips(n, flag, same_bits=True, **kw):
             o, lse = torch.full_like(ref[0], 7.0), torch.full_like(ref[1], 7.0)
