@@ -41,6 +41,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     asm("{\n.reg .b16 t;\ncvt.u16.u32 t, %1;\ncvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
     return r;
 }
+// Four e4m3 bytes to two pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     const uint32_t h = e4m3x2_to_f16x2(two);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));

@@ -70,6 +70,8 @@ extern "C" sr_status sr_paged_attention(const sr_paged_attention_args *a, void *
     p.scale_log2 = (a->scale != 0.f ? a->scale : 1.f / sqrtf(float(a->head_dim))) * 1.44269504088896341f;
     p.n_seqs = a->n_seqs, p.total = a->total_tokens, p.max_len = a->max_seqlen, p.max_kv = a->max_kvlen;
     p.h_q = a->h_q, p.h_kv = a->h_kv, p.group = a->h_q / a->h_kv;
+    p.group_inverse = p.group == 1 ? 0u : uint32_t(((1ull << 32) + p.group - 1) / p.group);
+    p.page_shift = a->page_size == 16 ? 4 : a->page_size == 32 ? 5 : a->page_size == 64 ? 6 : 7;
     p.page = a->page_size, p.n_pages = a->n_pages, p.max_pages = a->max_pages;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader + paged::tickets_bytes(), st);

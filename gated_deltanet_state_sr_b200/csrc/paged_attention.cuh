@@ -22,7 +22,8 @@ struct AttnParams {
     float *parts;     // partial O
     float2 *part_ml;  // their m and l
     float scale_log2; // scale log2(e)
-    int n_seqs, total, max_len, max_kv, h_q, h_kv, group, page, n_pages, max_pages;
+    int n_seqs, total, max_len, max_kv, h_q, h_kv, group, page, page_shift, n_pages, max_pages;
+    uint32_t group_inverse;  // ceil(2^32 / group): x / group = high half of x * it, for x group < 2^32
 };
 
 // Both kernels run one CTA per SM.
@@ -47,12 +48,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// Power of two that brings a row whose largest element is `top` to at most 1.
+// Power of two that brings a row whose largest element is `top` (not negative) to at most 1: its exponent's
+// negative, kept where a float has it; 1 for a row that is not finite.
 __device__ __forceinline__ float row_down(float top) {
-    if (!(top > 0.f) || top > 3.402823466e38f) return 1.f;
-    int e;
-    frexpf(top, &e);
-    return ldexpf(1.f, -min(max(e, -100), 120));
+    const int e = int(__float_as_uint(top) >> 23);  // biased exponent: top < 2^(e - 126)
+    return e == 255 ? 1.f : __uint_as_float(uint32_t(min(max(253 - e, 1), 227)) << 23);
 }
 // A block's scale, within the range that sr_kv_append writes; NaN becomes the least.
 __device__ __forceinline__ float usable_scale(float s) { return fminf(fmaxf(s, 0x1p-32f), 0x1p32f); }
@@ -65,16 +65,23 @@ __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return ((w & 0x7f7f7f
 __device__ __forceinline__ bool has_nan(uint32_t w) { return nan_bits(w) != 0; }
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_bits(w) >> 7) * 0xffu); }
 
-// The work of a call as one line of blocks, of which every CTA takes an equal
-// part.  A unit is ROWS query rows (row = token * group + head of the group) of a
+// The work of a call as one line, of which every CTA takes an equal part.  A
+// unit is ROWS query rows (row = token * group + head of the group) of a
 // (sequence, key/value head); it has one block for every TOK cached tokens that
-// its last row sees (one at least: rows that see nothing are written too).
-// Units of a sequence follow one another head by head, tile by tile.
+// its last row sees.  Units of a sequence follow one another head by head, tile
+// by tile.  On the line tile r of a sequence has a length in closed form, about
+// the cached tokens that it sees times the group, and a constant for what a unit
+// costs beside its blocks:
+//     length(r) = START + (cached before the new tokens) group + (r + 1) ROWS,
+// so that the place of every tile follows from a sum.  Offset x of a tile is its
+// block floor(x blocks / length): a cut falls on the same block for the CTA that
+// ends there and the one that begins there.
 struct Segment {
     int seq, head, tile, rows;   // rows: of this tile
-    int b0, b1, blocks;          // this CTA's blocks of the unit, and how many it has
+    int b0, b1;                  // this CTA's blocks of the unit
     int bos, count, kv;          // the sequence: first row, new tokens, cached tokens
-    int first_cta, last_cta;     // CTAs that hold the unit's blocks
+    bool whole;                  // the CTA has all of the unit
+    long long first, length;     // the unit's place on the line
 };
 
 struct LinePlace {
@@ -82,19 +89,16 @@ struct LinePlace {
     int seq;
 };
 
-template <int ROWS, int TOK> struct Line {
+template <int ROWS, int TOK, int START> struct Line {
     const AttnParams *p;
-    long long cur, end, total;
-    int ctas, seq, bos, count, kv, tiles, head, tile, block;
+    long long cur, end, total, at, per_head;  // at: where the current head's tiles begin
+    int ctas, seq, bos, count, kv, tiles, head, tile;
 
-    __device__ __forceinline__ int seen_by(int r) const {  // tokens that the last row of tile r sees
-        const int last = min((r + 1) * ROWS, count * p->group) - 1;
-        return max(0, kv - count + last / p->group + 1);
-    }
-    __device__ __forceinline__ int blocks_of(int r) const { return max(1, (seen_by(r) + TOK - 1) / TOK); }
+    __device__ __forceinline__ long long lead() const { return (long long)START + (long long)max(0, kv - count) * p->group; }
+    __device__ __forceinline__ long long tiles_length(int n) const { return n * lead() + (long long)ROWS * n * (n + 1) / 2; }
 
-    // Sequence n; the blocks of one of its heads, 0 where its entries are out of range (or it has no rows).
-    __device__ long long load(int n, bool flag) {
+    // Sequence n; the length of one of its heads, 0 where its entries are out of range (or it has no rows).
+    __device__ __forceinline__ long long load(int n, bool flag) {
         int b = p->cu[n], e = p->cu[n + 1], k = p->kv_lens[n];
         uint32_t bad = 0;
         if (b < 0 || b > e || e > p->total || (n == 0 && b != 0)) bad = SR_DEV_BAD_CU_SEQLENS;
@@ -106,29 +110,30 @@ template <int ROWS, int TOK> struct Line {
         }
         bos = b, count = e - b, kv = k;
         tiles = (count * p->group + ROWS - 1) / ROWS;
-        long long sum = 0;
-        for (int r = 0; r < tiles; ++r) sum += blocks_of(r);
-        return sum;
+        return tiles_length(tiles);
     }
 
-    // Finds the part of this CTA; all `THREADS` threads of the block call it.  False: there is none.
-    template <int THREADS> __device__ bool start(const AttnParams &params, int min_blocks, LinePlace &place) {
+    // Finds the part of this CTA, of at least `least` of the line; all `THREADS` threads of the block call it.  False:
+    // there is none.
+    template <int THREADS> __device__ bool start(const AttnParams &params, long long least, LinePlace &place) {
         p = &params;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         long long mine = 0;
+#pragma unroll 1
         for (int n = threadIdx.x; n < p->n_seqs; n += THREADS) mine += load(n, blockIdx.x == 0) * p->h_kv;
 #pragma unroll
         for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
         if (lane == 0) place.scan[warp] = mine;
         __syncthreads();
         total = 0;
+#pragma unroll 1
         for (int w = 0; w < THREADS / 32; ++w) total += place.scan[w];
         if (total == 0) return false;
-        ctas = int(min((long long)gridDim.x, (total + min_blocks - 1) / min_blocks));
+        ctas = int(min((long long)gridDim.x, (total + least - 1) / least));
         if (int(blockIdx.x) >= ctas) return false;
         cur = blockIdx.x * total / ctas;
         end = (blockIdx.x + 1) * total / ctas;
-        // the sequence that holds block `cur`: sums over THREADS sequences at a time
+        // the sequence that holds `cur`: sums over THREADS sequences at a time
         long long before = 0;
         for (int n0 = 0; before <= cur; n0 += THREADS) {
             const int n = n0 + threadIdx.x;
@@ -142,53 +147,71 @@ template <int ROWS, int TOK> struct Line {
             __syncthreads();
             if (lane == 31) place.scan[warp] = incl;
             __syncthreads();
-            long long at = before + incl - c, chunk = 0;
+            long long from = before + incl - c, chunk = 0;
+#pragma unroll 1
             for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < warp) at += place.scan[w];
+                if (w < warp) from += place.scan[w];
                 chunk += place.scan[w];
             }
-            if (c > 0 && cur >= at && cur < at + c) place.seq = n, place.at = at;
+            if (c > 0 && cur >= from && cur < from + c) place.seq = n, place.at = from;
             before += chunk;
         }
         __syncthreads();
         seq = place.seq;
-        const long long per_head = load(seq, false);
-        long long local = cur - place.at;
-        head = int(local / per_head);
-        local -= head * per_head;
-        for (tile = 0; local >= blocks_of(tile); ++tile) local -= blocks_of(tile);
-        block = int(local);
+        per_head = load(seq, false);
+        head = int((cur - place.at) / per_head);
+        at = place.at + head * per_head;
+        int lo = 0, hi = tiles - 1;  // the last tile that begins at or before cur
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (tiles_length(mid) <= cur - at) lo = mid; else hi = mid - 1;
+        }
+        tile = lo;
         return true;
     }
 
-    __device__ bool next(Segment &s) {
+    __device__ __forceinline__ bool next(Segment &s) {
         if (cur >= end) return false;
-        const int blocks = blocks_of(tile);
-        const int n = int(min((long long)(blocks - block), end - cur));
         s.seq = seq, s.head = head, s.tile = tile;
         s.rows = min(ROWS, count * p->group - tile * ROWS);
-        s.b0 = block, s.b1 = seen_by(tile) > 0 ? block + n : block, s.blocks = blocks;
         s.bos = bos, s.count = count, s.kv = kv;
-        const long long first = cur - block;
-        s.first_cta = int(((first + 1) * ctas - 1) / total);
-        s.last_cta = int(((first + blocks) * ctas - 1) / total);
-        cur += n;
-        block += n;
-        if (block == blocks) {
-            block = 0;
-            if (++tile == tiles) {
-                tile = 0;
-                if (++head == p->h_kv) {
-                    head = 0;
-                    if (cur < end)
-                        while (load(++seq, false) == 0) {
-                        }
-                }
+        s.first = at + tiles_length(tile);
+        s.length = lead() + (long long)(tile + 1) * ROWS;
+        const int seen = max(0, kv - count + (tile * ROWS + s.rows - 1) / p->group + 1);
+        const int blocks = (seen + TOK - 1) / TOK;
+        const long long x0 = cur - s.first, x1 = min(s.length, end - s.first);
+        s.whole = x0 == 0 && x1 == s.length;
+        s.b0 = x0 == 0 ? 0 : int(x0 * blocks / s.length);
+        s.b1 = x1 == s.length ? blocks : int(x1 * blocks / s.length);
+        cur = s.first + x1;
+        if (x1 == s.length && ++tile == tiles) {
+            tile = 0;
+            at += per_head;
+            if (++head == p->h_kv) {
+                head = 0;
+                if (cur < end)
+                    do per_head = load(++seq, false);
+                    while (per_head == 0);
             }
         }
         return true;
     }
+
+    // CTAs that hold the first and the last of a unit's places
+    __device__ __forceinline__ int first_cta(const Segment &s) const { return int(((s.first + 1) * ctas - 1) / total); }
+    __device__ __forceinline__ int last_cta(const Segment &s) const { return int(((s.first + s.length) * ctas - 1) / total); }
 };
+
+// tc::mbar_wait in few instructions: these kernels have a dozen places that wait, and what they run has to stay in the
+// instruction cache.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t phase) {
+    if (tc::mbar_try_wait(bar, phase)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t i = 1; !tc::mbar_try_wait(bar, phase); ++i)
+        if (i % 32 == 0 && tc::globaltimer_ns() - t0 > tc::kWaitLimitNs) return false;
+    return true;
+}
 
 // Tokens that row r of a segment's tile sees.
 __device__ __forceinline__ int line_seen(const AttnParams &p, const Segment &s, int r, int rows) {

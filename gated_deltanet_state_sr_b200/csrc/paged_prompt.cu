@@ -16,13 +16,16 @@
 //               range: many small weights beside a large one add up.
 // A CTA walks its part of the line of blocks (paged_attention.cuh).  Its warps:
 //   two groups of four: softmax, a row per thread, for two tiles of query rows
-//     (head dimension 256: one tile, whose scores have two buffers; its second
-//     group is idle), and the queries' split at the start of a unit;
+//     (head dimension 256: one tile, whose scores have two buffers; the groups
+//     take half of a tile's columns each and exchange the rows' largest), and the
+//     queries' split at the start of a unit;
 //   one group of four: values to half precision;
 //   a warp that issues the products, S of two items ahead of P V of one;
-//   a warp that loads pages.
+//   a warp that loads pages of keys, and one for values.
 // Tensor memory: two buffers of scores (128 columns each) and the sums O (two
 // times 128 columns, or 256).
+#include <type_traits>
+
 #include "paged_attention.cuh"
 
 namespace sr {
@@ -33,8 +36,9 @@ constexpr int kThreads = 512;
 constexpr int kTok = 128;       // cached tokens per tile
 constexpr int kHalf = 64;       // tokens per stage of values
 constexpr int kMinBlocks = 2;   // least tiles worth a CTA of their own
-// 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128, what the block is launched with.
-constexpr int kSoftmaxRegs = 184, kConvertRegs = 96, kIssueRegs = 48;
+constexpr int kUnitStart = 512; // what a unit costs beside its tokens, in tokens of one head
+// 256 x 160 + 128 x 96 + 128 x 96 = 512 x 128, what the block is launched with.
+constexpr int kSoftmaxRegs = 160, kConvertRegs = 96, kIssueRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= 512 * 128, "the split draws on the launch's");
 constexpr int kPoisonSlots = 16;
 
@@ -57,12 +61,17 @@ template <int D> struct PromptSmem {
         uint64_t raw_full[kRawStages], raw_empty[kRawStages];
         uint64_t v_full[kVStages], v_empty[kVStages];
         uint64_t s_full[2], p_full[2], pv_done[2];
-        LinePlace place;
+        union {
+            LinePlace place;            // at the start
+            float top[2][2][128];       // where two threads share a row: what they exchange
+        };
         uint32_t tmem;
         int poison[kPoisonSlots];
+        float row_scale[kTiles][128];
         int ticket[2];
     };
-    static constexpr int bytes = off_misc + int(sizeof(Misc)) + 1024;
+    static constexpr int bytes = off_misc + int(sizeof(Misc));
+    static_assert(bytes <= 227 * 1024, "what a block may have");
 };
 
 __device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t addr) {
@@ -89,25 +98,23 @@ template <int D> constexpr uint32_t idesc_pv() {
     return (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
 
-template <int GROUP> __device__ __forceinline__ void group_sync() {
-    asm volatile("bar.sync %0, 128;\n" ::"n"(GROUP) : "memory");
+__device__ __forceinline__ void named_sync(int id, int count) {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
 }
-__device__ __forceinline__ void softmax_sync(int group) {
-    if (group) group_sync<2>(); else group_sync<1>();
-}
-__device__ __forceinline__ bool softmax_or(int group, bool x) {
+__device__ __forceinline__ bool named_or(int id, int count, bool x) {
     int r;
-    if (group)
-        asm volatile("{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\nbar.red.or.pred q, 2, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
-                     : "=r"(r) : "r"(int(x)) : "memory");
-    else
-        asm volatile("{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\nbar.red.or.pred q, 1, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
-                     : "=r"(r) : "r"(int(x)) : "memory");
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.s32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"(id), "r"(count), "r"(int(x))
+                 : "memory");
     return r != 0;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 r;
@@ -116,8 +123,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 
 __device__ __forceinline__ int page_at(const AttnParams &p, int seq, int token) {
-    const int page = p.table[(long long)seq * p.max_pages + token / p.page];
+    const int page = p.table[(long long)seq * p.max_pages + (token >> p.page_shift)];
     return page < 0 || page >= p.n_pages ? 0 : page;  // the output of such a sequence is not written
+}
+
+// Which of the columns c .. c + 31 hold a NaN among tokens t0 .. t1 - 1.
+__device__ __forceinline__ uint32_t nan_columns(const AttnParams &p, const Segment &seg, int t0, int t1, int c, int d) {
+    uint32_t hit = 0;
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t) {
+        const uint8_t *v = p.v_cache + (((long long)page_at(p, seg.seq, t) * p.h_kv + seg.head) * p.page + t % p.page) * d + c;
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) hit |= uint32_t((v[e] & 127) == 127) << e;
+    }
+    return hit;
 }
 
 template <int D>
@@ -126,24 +145,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ AttnParams p) {
     using S = PromptSmem<D>;
     constexpr int NQ = S::kTiles;
-    extern __shared__ uint8_t raw_smem[];
-    uint8_t *smem = raw_smem + ((1024 - (tc::smem_u32(raw_smem) & 1023)) & 1023);
+    constexpr bool kSplit = NQ == 1;  // both softmax groups work on the one query tile
+    extern __shared__ __align__(1024) uint8_t smem[];
     typename S::Misc &misc = *reinterpret_cast<typename S::Misc *>(smem + S::off_misc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = tc::smem_u32(smem);
 
     if (threadIdx.x == 0) {
-        tc::mbar_init(&misc.q_full, 128 * NQ);
-        tc::mbar_init(&misc.o_free, 128 * NQ);
+        tc::mbar_init(&misc.q_full, 256);
+        tc::mbar_init(&misc.o_free, 256);
         for (int i = 0; i < S::kKStages; ++i) tc::mbar_init(&misc.k_full[i], 1), tc::mbar_init(&misc.k_empty[i], 1);
         for (int i = 0; i < S::kRawStages; ++i) tc::mbar_init(&misc.raw_full[i], 1), tc::mbar_init(&misc.raw_empty[i], 128);
         for (int i = 0; i < S::kVStages; ++i) tc::mbar_init(&misc.v_full[i], 128), tc::mbar_init(&misc.v_empty[i], 1);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&misc.s_full[i], 1), tc::mbar_init(&misc.p_full[i], 128), tc::mbar_init(&misc.pv_done[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&misc.s_full[i], 1), tc::mbar_init(&misc.p_full[i], kSplit ? 256 : 128), tc::mbar_init(&misc.pv_done[i], 1);
         for (int i = 0; i < kPoisonSlots; ++i) misc.poison[i] = 0;
         tc::fence_mbar_init();
     }
-    Line<S::kRows, kTok> line;
-    if (!line.template start<kThreads>(p, kMinBlocks, misc.place)) return;
+    Line<S::kRows, kTok, kUnitStart> line;
+    if (!line.template start<kThreads>(p, (long long)kMinBlocks * kTok * p.group, misc.place)) return;
     if (warp == 12) {
         tc::tmem_alloc(&misc.tmem, 512);
         tc::tmem_relinquish();
@@ -155,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment seg;
     bool alive = true;  // a wait that ran out ends a role; the others' waits then run out too
     auto wait = [&](uint64_t &bar, int phase) {
-        if (alive && !tc::mbar_wait(&bar, phase & 1)) {
+        if (alive && !wait_for(&bar, phase & 1)) {
             atomicOr(p.status, SR_DEV_TIMEOUT);
             alive = false;
         }
@@ -177,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tc_fence_after();
                     const uint32_t d = tmem + ((w + i) & 1) * 128;
                     uint32_t on = 0;
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int s = 0; s < D / 32; ++s) {
@@ -190,72 +209,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j == NQ - 1) tc::mma_commit(&misc.k_empty[st]);
                     return true;
                 };
-                for (int i = 0; i < 2 && i < items; ++i)
-                    if (!scores(i)) break;
-                if (unit && !wait(misc.o_free, unit - 1)) break;
-                for (int i = 0; alive && i < items; ++i) {
-                    const int tile = i / NQ, j = i - tile * NQ, b = (w + i) & 1;
-                    if (!wait(misc.p_full[b], (w + i) >> 1)) break;
+                // S of two items ahead of P V of one
+#pragma unroll 1
+                for (int i = 0; i < items + 2; ++i) {
+                    if (i >= 2) {
+                        const int tile = (i - 2) / NQ, j = (i - 2) - tile * NQ, b = (w + i) & 1;
+                        if (i == 2 && unit && !wait(misc.o_free, unit - 1)) break;
+                        if (!wait(misc.p_full[b], (w + i - 2) >> 1)) break;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int n = vt + tile * 2 + h, st = n % S::kVStages;
+                            if (!wait(misc.v_full[st], n / S::kVStages)) break;
+                            tc::tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = vt + tile * 2 + h, st = n % S::kVStages;
-                        if (!wait(misc.v_full[st], n / S::kVStages)) break;
-                        tc::tc_fence_after();
-#pragma unroll
-                        for (int s = 0; s < kHalf / 16; ++s)
-                            mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * 32 + s * 8,
-                                       tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
-                                       idesc_pv<D>(), tile | h | s ? 1u : 0u);
-                        if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
+                            for (int s = 0; s < kHalf / 16; ++s)
+                                mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * (kSplit ? 64 : 32) + s * 8,
+                                           tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
+                                           idesc_pv<D>(), tile | h | s ? 1u : 0u);
+                            if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
+                        }
+                        if (!alive) break;
+                        tc::mma_commit(&misc.pv_done[b]);
                     }
-                    if (!alive) break;
-                    tc::mma_commit(&misc.pv_done[b]);
-                    if (i + 2 < items && !scores(i + 2)) break;
+                    if (i < items && !scores(i)) break;
                 }
+                // a unit without tiles keeps the count of the sums' releases
+                if (items == 0 && unit && !wait(misc.o_free, unit - 1)) break;
                 kt += tiles, vt += 2 * tiles, w += items;
             }
         } else if (warp == 13) {
-            // ---- loads: a page (64 rows of it at most) per lane
-            int kt = 0, vt = 0;
+            // ---- keys: a page (64 rows of it at most) per lane; pages behind the sequence's end are not read
+            int kt = 0;
             const int rows = min(p.page, 64);
-            while (line.next(seg)) {
+            while (line.next(seg))
                 for (int b = seg.b0; b < seg.b1; ++b, ++kt) {
-                    const int ks = kt % S::kKStages;
-                    const int left = seg.kv - b * kTok;                      // tokens from here on
-                    const int pieces = (min(kTok, left) + rows - 1) / rows;  // pages behind the end are not read
-                    const int at = b * kTok + lane * rows;
-                    int y = 0;
+                    const int st = kt % S::kKStages, at = b * kTok + lane * rows;
+                    const int pieces = (min(kTok, seg.kv - b * kTok) + rows - 1) / rows;
+                    int y = 0, ok = 1;
                     if (lane < pieces) y = (page_at(p, seg.seq, at) * p.h_kv + seg.head) * p.page + at % p.page;
-                    int ok = 1;
                     if (lane == 0) {
-                        ok = kt < S::kKStages || wait(misc.k_empty[ks], kt / S::kKStages - 1);
-                        if (ok) tc::mbar_arrive_expect_tx(&misc.k_full[ks], pieces * rows * D);
+                        ok = kt < S::kKStages || wait(misc.k_empty[st], kt / S::kKStages - 1);
+                        if (ok) tc::mbar_arrive_expect_tx(&misc.k_full[st], pieces * rows * D);
                     }
                     if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
                     if (lane < pieces)
 #pragma unroll
                         for (int x = 0; x < S::kSubs; ++x)
-                            tc::tma_load_2d(smem + S::off_k + ks * S::kK + x * kTok * 128 + lane * rows * S::kSub, &kmap,
-                                            &misc.k_full[ks], x * 128, y);
-                    const int per = kHalf / rows;  // pieces per stage of values
-#pragma unroll
-                    for (int h = 0; h < 2; ++h, ++vt) {
-                        const int vs = vt % S::kRawStages;
-                        const int mine = min(max(pieces - h * per, 0), per);
-                        if (lane == 0) {
-                            ok = vt < S::kRawStages || wait(misc.raw_empty[vs], vt / S::kRawStages - 1);
-                            if (ok) tc::mbar_arrive_expect_tx(&misc.raw_full[vs], mine * rows * D);
-                        }
-                        if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
-                        const int l = lane - h * per;
-                        if (l >= 0 && l < mine)
-#pragma unroll
-                            for (int x = 0; x < S::kSubs; ++x)
-                                tc::tma_load_2d(smem + S::off_raw + vs * S::kRaw + x * kHalf * 128 + l * rows * S::kSub,
-                                                &vmap, &misc.raw_full[vs], x * 128, y);
-                    }
+                            tc::tma_load_2d(smem + S::off_k + st * S::kK + x * kTok * 128 + lane * rows * S::kSub, &kmap,
+                                            &misc.k_full[st], x * 128, y);
                 }
-            }
+        } else if (warp == 14) {
+            // ---- values, a warp of their own: a wait for either ring would hold up the other
+            int vt = 0;
+            const int rows = min(p.page, 64);
+            while (line.next(seg))
+                for (int t0 = seg.b0 * kTok; t0 < seg.b1 * kTok; t0 += kHalf, ++vt) {
+                    const int st = vt % S::kRawStages, at = t0 + lane * rows;
+                    const int pieces = (min(kHalf, max(0, seg.kv - t0)) + rows - 1) / rows;
+                    int y = 0, ok = 1;
+                    if (lane < pieces) y = (page_at(p, seg.seq, at) * p.h_kv + seg.head) * p.page + at % p.page;
+                    if (lane == 0) {
+                        ok = vt < S::kRawStages || wait(misc.raw_empty[st], vt / S::kRawStages - 1);
+                        if (ok) tc::mbar_arrive_expect_tx(&misc.raw_full[st], pieces * rows * D);
+                    }
+                    if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
+                    if (lane < pieces)
+#pragma unroll
+                        for (int x = 0; x < S::kSubs; ++x)
+                            tc::tma_load_2d(smem + S::off_raw + st * S::kRaw + x * kHalf * 128 + lane * rows * S::kSub, &vmap,
+                                            &misc.raw_full[st], x * 128, y);
+                }
         }
     } else if (warp >= 8) {
         // ---- values to half precision: token rows of 64 columns, 128-byte swizzle, the layout of an MN-major operand
@@ -264,161 +287,207 @@ __global__ void __launch_bounds__(kThreads, 1)
         int vt = 0;
         for (int unit = 0; alive && line.next(seg); ++unit) {
             const int most = line_seen(p, seg, seg.rows - 1, S::kRows), least = line_seen(p, seg, 0, S::kRows);
-            for (int b = seg.b0; b < seg.b1 && alive; ++b)
-                for (int h = 0; h < 2; ++h, ++vt) {
-                    const int rs = vt % S::kRawStages, vs = vt % S::kVStages, tok0 = b * kTok + h * kHalf;
-                    if (!wait(misc.raw_full[rs], vt / S::kRawStages)) break;
-                    if (vt >= S::kVStages && !wait(misc.v_empty[vs], vt / S::kVStages - 1)) break;
-                    const uint32_t src = base + S::off_raw + rs * S::kRaw, dst = base + S::off_v + vs * S::kV;
-                    const bool end = tok0 + kHalf > most;    // tokens that nobody sees
-                    const bool edge = tok0 + kHalf > least;  // tokens that some rows see and others do not
-                    constexpr int kChunks = D / 16;          // 16-byte chunks of a row
+#pragma unroll 1
+            for (int tok0 = seg.b0 * kTok; tok0 < seg.b1 * kTok; tok0 += kHalf, ++vt) {
+                const int rs = vt % S::kRawStages, vs = vt % S::kVStages;
+                if (!wait(misc.raw_full[rs], vt / S::kRawStages)) break;
+                if (vt >= S::kVStages && !wait(misc.v_empty[vs], vt / S::kVStages - 1)) break;
+                const uint32_t src = base + S::off_raw + rs * S::kRaw, dst = base + S::off_v + vs * S::kV;
+                constexpr int kChunks = D / 16;               // 16-byte chunks of a row
+                constexpr int kMine = kHalf * kChunks / 128;  // of them this thread's
+                constexpr int kBatch = kMine < 4 ? kMine : 4; // loaded before the first is converted
+                if (tok0 + kHalf > least) {
+                    // Tokens that nobody sees become zeros; where rows see different ones, a NaN is left to the end of
+                    // the sums.  In place and apart from the conversions, which a branch would keep from overlapping.
                     bool poison = false;
-#pragma unroll
-                    for (int i = 0; i < kHalf * kChunks / 128; ++i) {
-                        const int x = i * 128 + t, r = x / kChunks, c = x % kChunks;
-                        uint4 v = lds128(src + chunk8_at<D>(kHalf, r, c));
-                        if (end && tok0 + r >= most) v = make_uint4(0, 0, 0, 0);
-                        if (edge && (has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w))) {
-                            poison = true;
-                            v.x = without_nan(v.x), v.y = without_nan(v.y), v.z = without_nan(v.z), v.w = without_nan(v.w);
-                        }
-                        const uint32_t row = dst + (c >> 2) * (kHalf * 128) + r * 128;
-                        // lanes of the two 64-column blocks write their halves in opposite orders: no bank conflicts
-                        const int first = (c >> 2) & 1;
-                        const uint32_t a0 = e4m3x2_to_f16x2(v.x), a1 = e4m3x2_to_f16x2(v.x >> 16);
-                        const uint32_t a2 = e4m3x2_to_f16x2(v.y), a3 = e4m3x2_to_f16x2(v.y >> 16);
-                        const uint32_t b0 = e4m3x2_to_f16x2(v.z), b1 = e4m3x2_to_f16x2(v.z >> 16);
-                        const uint32_t b2 = e4m3x2_to_f16x2(v.w), b3 = e4m3x2_to_f16x2(v.w >> 16);
-                        const int c0 = (c & 3) * 2;
-                        const uint32_t at0 = row + (((c0 + first) ^ (r & 7)) << 4), at1 = row + (((c0 + 1 - first) ^ (r & 7)) << 4);
-                        if (first) {
-                            sts128(at0, b0, b1, b2, b3);
-                            sts128(at1, a0, a1, a2, a3);
-                        } else {
-                            sts128(at0, a0, a1, a2, a3);
-                            sts128(at1, b0, b1, b2, b3);
-                        }
+#pragma unroll 1
+                    for (int i = 0; i < kMine; ++i) {
+                        const int x = i * 128 + t;
+                        const uint32_t at = src + chunk8_at<D>(kHalf, x / kChunks, x % kChunks);
+                        uint4 v = lds128(at);
+                        if (tok0 + x / kChunks >= most) v = make_uint4(0, 0, 0, 0);
+                        poison |= has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w);
+                        sts128(at, without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
                     }
                     if (poison) misc.poison[unit % kPoisonSlots] = unit + 1;
-                    tc::fence_async_smem();
-                    tc::mbar_arrive(&misc.v_full[vs]);
-                    tc::mbar_arrive(&misc.raw_empty[rs]);
                 }
+#pragma unroll 1
+                for (int i0 = 0; i0 < kMine; i0 += kBatch) {
+                    uint4 in[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int x = (i0 + i) * 128 + t;
+                        in[i] = lds128(src + chunk8_at<D>(kHalf, x / kChunks, x % kChunks));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int x = (i0 + i) * 128 + t, r = x / kChunks, c = x % kChunks;
+                        const uint4 v = in[i];
+                        // lanes of neighbouring 64-column blocks write their halves in opposite orders, so that no two
+                        // meet in a bank
+                        const bool odd = (c >> 2) & 1;
+                        const uint2 lo = odd ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+                        const uint2 hi = odd ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
+                        const uint32_t row = dst + (c >> 2) * (kHalf * 128) + r * 128;
+                        const uint32_t at = row + ((((c & 3) * 2 + odd) ^ (r & 7)) << 4);
+                        uint32_t f[4];
+                        e4m3x4_to_f16x4(lo.x, f[0], f[1]);
+                        e4m3x4_to_f16x4(lo.y, f[2], f[3]);
+                        sts128(at, f[0], f[1], f[2], f[3]);
+                        e4m3x4_to_f16x4(hi.x, f[0], f[1]);
+                        e4m3x4_to_f16x4(hi.y, f[2], f[3]);
+                        sts128(at ^ 16, f[0], f[1], f[2], f[3]);
+                    }
+                }
+                tc::fence_async_smem();
+                tc::mbar_arrive(&misc.v_full[vs]);
+                tc::mbar_arrive(&misc.raw_empty[rs]);
+            }
         }
     } else {
-        // ---- softmax: a query row per thread
+        // ---- softmax: a query row per thread; at head dimension 256 two threads, each half of a tile's columns and of O's
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-        const int group = warp >> 2;  // query tile
+        constexpr int kCols = kSplit ? kTok / 2 : kTok, kOut = kSplit ? D / 2 : D, kChunks = kCols / 32;
+        const int group = warp >> 2, q_tile = kSplit ? 0 : group;
         const int row = threadIdx.x & 127;
+        const int col0 = kSplit ? group * kCols : 0, out0 = kSplit ? group * kOut : 0;
+        const int bar_id = kSplit ? 1 : 1 + group, bar_count = kSplit ? 256 : 128;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+        const uint32_t o_at = tmem + lanes + 256 + q_tile * 128 + out0;
         int w = 0;       // items of the CTA so far
         int checked = -1;
         bool bad_pages = false;
-        for (int unit = 0; group < NQ && alive && line.next(seg); ++unit) {
+        for (int unit = 0; alive && line.next(seg); ++unit) {
             const int tiles = seg.b1 - seg.b0;
-            const int r = group * 128 + row, g = seg.tile * S::kRows + r, token = g / p.group;
+            // the tile's first row's token and head of the group, and from there those of row x
+            const int g0 = seg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
+            auto place = [&](int x, int &token, int &h) {
+                const int y = head0 + x, up = p.group == 1 ? y : int(__umulhi(uint32_t(y), p.group_inverse));
+                token = token0 + up, h = seg.head * p.group + (y - up * p.group);
+            };
+            const int r = q_tile * 128 + row;
+            int token, head;
+            place(r, token, head);
             const bool real = r < seg.rows;
             const int seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
             if (checked != seg.seq) {
                 bool bad = false;
-                const int pages = (seg.kv + p.page - 1) / p.page;
-                for (int i = row; i < pages; i += 128) {
+                const int pages = (seg.kv + p.page - 1) >> p.page_shift;
+                for (int i = kSplit ? threadIdx.x : row; i < pages; i += bar_count) {
                     const int page = p.table[(long long)seg.seq * p.max_pages + i];
                     bad |= page < 0 || page >= p.n_pages;
                 }
-                bad_pages = softmax_or(group, bad);
-                if (bad_pages && row == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
+                bad_pages = named_or(bar_id, bar_count, bad);
+                if (bad_pages && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
                 checked = seg.seq;
             }
-            // the row's query as hi + lo
+            // the queries as hi + lo: D / 8 lanes read a row, 16 bytes each
             float row_scale;
             {
-                const __nv_bfloat16 *src =
-                    p.q + (long long)(seg.bos + token) * p.q_stride + (seg.head * p.group + g % p.group) * D;
-                float top = 0.f;
-                if (real)
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = reinterpret_cast<const uint4 *>(src)[c];
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4, kMine = kSplit ? 16 : 32;
+                const int sub = lane / kLanes, c8 = lane % kLanes, row0 = kSplit ? warp * 16 : (warp & 3) * 32;
+                const uint32_t hi_at = base + q_tile * 2 * S::kQ, lo_at = hi_at + S::kQ;
+                float *scales = misc.row_scale[q_tile];
+                const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
+#pragma unroll 1
+                for (int i0 = 0; i0 < kMine; i0 += kAtOnce * kBatch) {
+                    uint4 in[kBatch];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u))));
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int x = q_tile * 128 + row0 + i0 + i * kAtOnce + sub;
+                        int tx, hx;
+                        place(x, tx, hx);
+                        in[i] = make_uint4(0, 0, 0, 0);
+                        if (x < seg.rows)
+                            in[i] = *reinterpret_cast<const uint4 *>(p.q + (long long)(seg.bos + tx) * p.q_stride + hx * D + 8 * c8);
                     }
-                const float down = row_down(top) * 256.f;
-                row_scale = p.scale_log2 / down;
-                const uint32_t hi_at = base + group * 2 * S::kQ, lo_at = hi_at + S::kQ;
-#pragma unroll 2
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint4 v = real ? reinterpret_cast<const uint4 *>(src)[2 * c + u] : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r_at = row0 + i0 + i * kAtOnce + sub;
+                        const uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                        float f[8], top = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+                            top = fmaxf(top, fabsf(f[e]));
+                        }
+#pragma unroll
+                        for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float down = row_down(top), factor = down * sign;
+                        uint32_t hi[2], lo[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float f0 = __uint_as_float(x[2 * e] << 16) * down, f1 = __uint_as_float(x[2 * e] & 0xffff0000u) * down;
-                            const float f2 = __uint_as_float(x[2 * e + 1] << 16) * down,
-                                        f3 = __uint_as_float(x[2 * e + 1] & 0xffff0000u) * down;
-                            const uint32_t h = to_e4m3x4(f0, f1, f2, f3);
-                            const float2 a = e4m3x2_to_float2(h), b = e4m3x2_to_float2(h >> 16);
-                            hi[2 * u + e] = h;
-                            lo[2 * u + e] = to_e4m3x4(f0 - a.x, f1 - a.y, f2 - b.x, f3 - b.y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
+                            hi[e] = to_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            const float2 a = e4m3x2_to_float2(hi[e]), b = e4m3x2_to_float2(hi[e] >> 16);
+                            lo[e] = to_e4m3x4(f[4 * e] - a.x, f[4 * e + 1] - a.y, f[4 * e + 2] - b.x, f[4 * e + 3] - b.y);
                         }
+                        const uint32_t at = chunk8_at<D>(128, r_at, c8 >> 1) + (c8 & 1) * 8;
+                        sts64(hi_at + at, hi[0], hi[1]);
+                        sts64(lo_at + at, lo[0], lo[1]);
+                        // the inverse of a power of two, by its exponent; every lane of the row writes the same
+                        scales[r_at] = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
                     }
-                    const uint32_t at = chunk8_at<D>(128, row, c);
-                    sts128(hi_at + at, hi[0], hi[1], hi[2], hi[3]);
-                    sts128(lo_at + at, lo[0], lo[1], lo[2], lo[3]);
                 }
                 tc::fence_async_smem();
                 tc::mbar_arrive(&misc.q_full);
+                if (kSplit) named_sync(bar_id, bar_count); else __syncwarp();
+                row_scale = scales[row];
             }
 
             float m = kNone, l = 0.f;
-            const uint32_t o_at = tmem + lanes + 256 + group * 128;
-            // lane g of every eight holds the scales of the tile's tokens 16 g .. 16 g + 15, loaded a tile ahead
-            auto scales_of = [&](int b, float &ks, float &vs) {
-                const int at = b * kTok + (lane & 7) * 16;
-                ks = vs = 1.f;
-                if (b < seg.b1 && at < seg.kv) {
-                    const long long block = (long long)page_at(p, seg.seq, at) * p.h_kv + seg.head;
-                    ks = p.k_scale[block], vs = p.v_scale[block];
+            // Lane g of every eight (four) holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
+            // columns, loaded a tile ahead, their page two.
+            auto page_of = [&](int b) {
+                const int at = b * kTok + col0 + (lane & (kCols / 16 - 1)) * 16;
+                return b < seg.b1 && at < seg.kv ? page_at(p, seg.seq, at) : -1;
+            };
+            float ks_next = 1.f, vs_next = 1.f;
+            auto load_scales = [&](int page) {
+                if (page >= 0) {
+                    const long long block = (long long)page * p.h_kv + seg.head;
+                    ks_next = p.k_scale[block], vs_next = p.v_scale[block];
                 }
             };
-            float ks_next, vs_next;
-            scales_of(seg.b0, ks_next, vs_next);
+            load_scales(page_of(seg.b0));
+            int page_next = page_of(seg.b0 + 1);
             for (int t = 0; t < tiles; ++t) {
-                const int item = w + t * NQ + group, buf = item & 1;
-                const int tok0 = (seg.b0 + t) * kTok;
+                const int item = w + t * NQ + q_tile, buf = item & 1;
+                const int tok0 = (seg.b0 + t) * kTok + col0;
                 const float ks = usable_scale(ks_next), vs = usable_scale(vs_next);
-                scales_of(seg.b0 + t + 1, ks_next, vs_next);
-                const float lv = log2f(vs), up = 1.f / vs;
+                load_scales(page_next);
+                page_next = page_of(seg.b0 + t + 2);
+                const float lv = __log2f(vs), up = __frcp_rn(vs);
+                const bool edge = __any_sync(0xffffffffu, tok0 + kCols > seen);
+                const uint32_t s_at = tmem + lanes + buf * 128 + col0;
                 if (!wait(misc.s_full[buf], item >> 1)) break;
                 tc::tc_fence_after();
-                const uint32_t s_at = tmem + lanes + buf * 128;
-                uint32_t x[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::tmem_ld_32x32b_x32(s_at + 32 * q, x[q]);
-                tc::tmem_ld_wait();
+                // Two passes over the scores, 32 at a time, so that registers hold no row of 128 and the loops stay in the
+                // instruction cache: the largest of every 16 (whose scales are alike), then the weights.
                 float top = -INFINITY;
-                const bool edge = __any_sync(0xffffffffu, tok0 + kTok > seen);
+#pragma unroll 1
+                for (int q = 0; q < kChunks; ++q) {
+                    uint32_t y[32];
+                    tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
+                    tc::tmem_ld_wait();
+                    if (edge)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float k = row_scale * __shfl_sync(0xffffffffu, ks, q), v = __shfl_sync(0xffffffffu, lv, q);
+                        for (int c = 0; c < 32; ++c) y[c] = tok0 + 32 * q + c < seen ? y[c] : 0xff800000u;  // -inf
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float s = fmaf(__uint_as_float(x[q >> 1][(q & 1) * 16 + c]), k, v);
-                        x[q >> 1][(q & 1) * 16 + c] = __float_as_uint(s);
+                    for (int h = 0; h < 2; ++h) {
+                        float most[2] = {__uint_as_float(y[16 * h]), __uint_as_float(y[16 * h + 1])};
+#pragma unroll
+                        for (int c = 2; c < 16; ++c) most[c & 1] = fmaxf(most[c & 1], __uint_as_float(y[16 * h + c]));
+                        const float k = row_scale * __shfl_sync(0xffffffffu, ks, 2 * q + h);
+                        top = fmaxf(top, fmaf(fmaxf(most[0], most[1]), k, __shfl_sync(0xffffffffu, lv, 2 * q + h)));
                     }
                 }
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < kTok; ++c)
-                        if (tok0 + c >= seen) x[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+                if (kSplit) {  // the other half's largest
+                    misc.top[buf][group][row] = top;
+                    named_sync(bar_id, bar_count);
+                    top = fmaxf(misc.top[buf][0][row], misc.top[buf][1][row]);
                 }
-#pragma unroll
-                for (int c = 0; c < kTok; ++c) top = fmaxf(top, __uint_as_float(x[c >> 5][c & 31]));
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     const float next = fmaxf(m, top), f = exp2f(m - next);
                     m = next, l *= f;
@@ -426,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(misc.pv_done[(item - NQ) & 1], (item - NQ) >> 1)) break;
                         tc::tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
+                        for (int c = 0; c < kOut; c += 32) {
                             uint32_t y[32];
                             tc::tmem_ld_32x32b_x32(o_at + c, y);
                             tc::tmem_ld_wait();
@@ -437,45 +506,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float z = m - kShift;
+                // weights of columns 32 q .., over 16 columns of the scores' own, all of them read already
+                auto weights_of = [&](const uint32_t(&y)[32], int q, auto masked) {
+                    uint32_t out[16];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t y[32];
+                    for (int h = 0; h < 2; ++h) {
+                        const float k = row_scale * __shfl_sync(0xffffffffu, ks, 2 * q + h);
+                        const float v = __shfl_sync(0xffffffffu, lv, 2 * q + h) - z;
+                        float sum[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            const int at = half * 64 + q * 16 + c;
-                            const float a = ex2(__uint_as_float(x[at >> 5][at & 31]) - z);
-                            const float b = ex2(__uint_as_float(x[at >> 5][(at & 31) + 1]) - z);
-                            sum += a + b;
-                            y[(q * 16 + c) / 2] = pack_f16(a, b);
+                        for (int c = 16 * h; c < 16 * h + 16; c += 2) {
+                            float a = ex2(fmaf(__uint_as_float(y[c]), k, v));
+                            float b = ex2(fmaf(__uint_as_float(y[c + 1]), k, v));
+                            if (masked) {
+                                a = tok0 + 32 * q + c < seen ? a : 0.f;
+                                b = tok0 + 32 * q + c + 1 < seen ? b : 0.f;
+                            }
+                            sum[0] += a, sum[1] += b;
+                            out[c / 2] = pack_f16(a, b);
                         }
-                        l = fmaf(sum, __shfl_sync(0xffffffffu, up, half * 4 + q), l);
+                        l = fmaf(sum[0] + sum[1], __shfl_sync(0xffffffffu, up, 2 * q + h), l);
                     }
-                    tc::tmem_st_32x32b_x32(s_at + 32 * half, y);
-                }
+                    tc::tmem_st_32x32b_x16(s_at + 16 * q, out);
+                };
+                auto weights = [&](auto masked) {
+#pragma unroll 1
+                    for (int q = 0; q < kChunks; ++q) {
+                        uint32_t y[32];
+                        tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
+                        tc::tmem_ld_wait();
+                        weights_of(y, q, masked);
+                    }
+                };
+                // two copies: with the test in the loop every pair of columns would be a block of its own
+                if (edge)
+                    weights(std::true_type{});
+                else
+                    weights(std::false_type{});
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&misc.p_full[buf]);
             }
-            const int last = w + (tiles - 1) * NQ + group;
+            const int last = w + (tiles - 1) * NQ + q_tile;
             w += tiles * NQ;
             if (!alive) break;
+            if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
+                float(*sums)[128] = misc.top[(last + 1) & 1];
+                sums[group][row] = l;
+                named_sync(bar_id, bar_count);
+                l = sums[0][row] + sums[1][row];
+            }
             if (tiles > 0 && !wait(misc.pv_done[last & 1], last >> 1)) break;
             tc::tc_fence_after();
 
             // ---- the unit's sums
-            const bool whole = seg.first_cta == seg.last_cta;
+            const int first_cta = seg.whole ? 0 : line.first_cta(seg), last_cta = seg.whole ? 0 : line.last_cta(seg);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long out_row = (long long)(seg.bos + token) * p.h_q + seg.head * p.group + g % p.group;
-            const int slot = 2 * blockIdx.x + (int(blockIdx.x) == seg.first_cta ? 1 : 0);
+            const long long out_row = (long long)(seg.bos + token) * p.h_q + head;
+            const int slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
             // part sums: [slot][tile][D / 4][128 rows] of four columns, so that neighbouring rows lie together
-            float4 *part = reinterpret_cast<float4 *>(p.parts) + (long long)(slot * NQ + group) * (D / 4) * 128 + row;
+            float4 *part = reinterpret_cast<float4 *>(p.parts) + ((long long)(slot * NQ + q_tile) * D + out0) / 4 * 128 + row;
             const bool poisoned = misc.poison[unit % kPoisonSlots] == unit + 1;
             const int edge0 = line_seen(p, seg, 0, S::kRows) / kHalf * kHalf;  // the first stage that rows see differently
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < kOut; c += 32) {
                 uint32_t y[32];
                 if (tiles > 0) {
                     tc::tmem_ld_32x32b_x32(o_at + c, y);
@@ -484,24 +578,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = 0;
                 }
-                if (poisoned && real && !bad_pages)
-                    for (int t = max(edge0, seg.b0 * kTok); t < min(seen, seg.b1 * kTok); ++t) {
-                        const uint8_t *v = p.v_cache + (((long long)page_at(p, seg.seq, t) * p.h_kv + seg.head) * p.page + t % p.page) * D + c;
+                if (poisoned && real && !bad_pages) {
+                    const uint32_t hit = nan_columns(p, seg, max(edge0, seg.b0 * kTok), min(seen, seg.b1 * kTok), out0 + c, D);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((v[e] & 127) == 127) y[e] = 0x7fc00000u;
+                    for (int e = 0; e < 32; ++e) y[e] = hit >> e & 1 ? 0x7fc00000u : y[e];
+                }
+                if (seg.whole) {
+                    // half of the thread's columns at a time, padded rows in the query tile's place, which no product
+                    // reads any more
+                    if (c % (kOut / 2) == 0) tc::bulk_wait_read();
+                    uint8_t *mine = smem + group * (kSplit ? 1 : 2) * S::kQ + row * (kOut + 16);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        sts128(tc::smem_u32(mine) + (c % (kOut / 2) + e) * 2,
+                               pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
+                    if ((c + 32) % (kOut / 2) == 0) {
+                        tc::fence_async_smem();
+                        if (real && !bad_pages)
+                            tc::bulk_store(p.o + out_row * D + out0 + (c >= kOut / 2 ? kOut / 2 : 0), mine, kOut);
+                        tc::bulk_commit();
                     }
-                if (whole) {
-                    if (real && !bad_pages)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 v;
-                            v.x = pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv);
-                            v.y = pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv);
-                            v.z = pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv);
-                            v.w = pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(p.o + out_row * D + c + e) = v;
-                        }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
@@ -511,24 +610,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::tc_fence_before();
             tc::mbar_arrive(&misc.o_free);
-            if (whole) {
-                if (real && !bad_pages && p.lse) p.lse[out_row] = log_sum(m, l);
+            if (seg.whole) {
+                if (real && !bad_pages && p.lse && out0 == 0) p.lse[out_row] = log_sum(m, l);
+                tc::bulk_wait_read();
+                named_sync(bar_id, bar_count);  // the rows' place is the queries' again
                 continue;
             }
-            p.part_ml[(slot * NQ + group) * 128 + row] = make_float2(m, l);
+            if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
             __threadfence();
-            softmax_sync(group);
-            if (row == 0) {
-                int *ticket = &p.tickets[seg.first_cta * NQ + group];
-                const bool mine = atomicAdd(ticket, 1) == seg.last_cta - seg.first_cta;
+            named_sync(bar_id, bar_count);
+            if (row == 0 && out0 == 0) {
+                int *ticket = &p.tickets[first_cta * NQ + q_tile];
+                const bool mine = atomicAdd(ticket, 1) == last_cta - first_cta;
                 if (mine) *ticket = 0;
                 __threadfence();
-                misc.ticket[group] = mine;
+                misc.ticket[q_tile] = mine;
             }
-            softmax_sync(group);
-            if (misc.ticket[group] && real && !bad_pages) {
-                const int parts = seg.last_cta - seg.first_cta + 1;
-                auto at = [&](int i) { return (2 * (seg.first_cta + i) + (i == 0)) * NQ + group; };
+            named_sync(bar_id, bar_count);
+            if (misc.ticket[q_tile] && real && !bad_pages) {
+                const int parts = last_cta - first_cta + 1;
+                auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
                 float M = kNone, L = 0.f;
                 for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
                 for (int i = 0; i < parts; ++i) {
@@ -537,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float one = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
-                for (int c = 0; c < D / 4; c += 8) {
+                for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
                     float4 sum[8] = {};
                     for (int i = 0; i < parts; ++i) {
                         const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
@@ -556,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
                                        pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
                 }
-                if (p.lse) p.lse[out_row] = log_sum(M, L);
+                if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
             }
-            softmax_sync(group);  // the ticket may be written again
+            named_sync(bar_id, bar_count);  // the ticket may be written again
         }
     }
 done:

@@ -42,6 +42,7 @@ constexpr int kLaunchRegs = 168, kLoadRegs = 40, kMathRegs = 232;
 static_assert(128 * kLoadRegs + 32 * kWarps * kMathRegs <= kThreads * kLaunchRegs, "the split draws on the launch's registers");
 constexpr int kTok = 64;               // tokens per stage: 4 warps of 16
 constexpr int kMinBlocks = 2;          // least blocks worth a CTA of their own
+constexpr int kUnitStart = 64;         // what a unit costs beside its tokens, in tokens of one head
 
 // Join barrier of the eight consumer warps.
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_mbar_init();
     }
-    Line<16, kTok> line;
-    if (!line.start<kThreads>(p, kMinBlocks, misc.place)) return;
+    Line<16, kTok, kUnitStart> line;
+    if (!line.start<kThreads>(p, (long long)kMinBlocks * kTok * p.group, misc.place)) return;
 
     const uint32_t stage0 = tc::smem_u32(smem);
     Segment seg;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rows = min(p.page, kTok);
                 bool ok = true;
                 if (lane == 0) {
-                    ok = it < kStages || tc::mbar_wait(&misc.empty[slot], ((it / kStages) - 1) & 1);
+                    ok = it < kStages || wait_for(&misc.empty[slot], ((it / kStages) - 1) & 1);
                     if (ok)
                         tc::mbar_arrive_expect_tx(&misc.full[slot], pieces * rows * D * 2);
                     else
@@ -236,13 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((it & 1) != (warp >> 2)) continue;
             const int slot = it % kStages;
             const int row0 = (warp & 3) * 16, tok0 = b * kTok + row0;
-            if (alive && !tc::mbar_wait(&misc.full[slot], (it / kStages) & 1)) {
+            if (alive && !wait_for(&misc.full[slot], (it / kStages) & 1)) {
                 if (lane == 0) atomicOr(p.status, SR_DEV_TIMEOUT);
                 alive = false;
             }
             if (tok0 < seen_most && alive) {
                 const uint32_t kt = stage0 + slot * 2 * S::kTile, vt = kt + S::kTile;
-                int page = p.table[(long long)seg.seq * p.max_pages + tok0 / p.page];
+                int page = p.table[(long long)seg.seq * p.max_pages + (tok0 >> p.page_shift)];
                 page = page < 0 || page >= p.n_pages ? 0 : page;
                 const long long block = (long long)page * p.h_kv + seg.head;
                 const float ks = usable_scale(p.k_scale[block]), vs = usable_scale(p.v_scale[block]);
@@ -258,7 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint4 a = *reinterpret_cast<const uint4 *>(qf + ((c * 4 + i) * 32 + lane) * 4);
-                            mma_f16(s[n], a, e4m3x2_to_f16x2(words[i]), e4m3x2_to_f16x2(words[i] >> 16));
+                            uint32_t b0, b1;
+                            e4m3x4_to_f16x4(words[i], b0, b1);
+                            mma_f16(s[n], a, b0, b1);
                         }
                     }
                 }
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const bool edge = tok0 + 16 > seen_least;
-                const float lvs = log2f(vs), k0 = c0 * ks, k1 = c1 * ks;
+                const float lvs = __log2f(vs), k0 = c0 * ks, k1 = c1 * ks;
                 float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[n][e] = ex2(s[n][e] - z0);
                         s[n][2 + e] = ex2(s[n][2 + e] - z1);
                     }
-                const float up = 1.f / vs;
+                const float up = __frcp_rn(vs);
                 l0 = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), up, l0);
                 l1 = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), up, l1);
                 const uint4 a = make_uint4(pack_f16(s[0][0], s[0][1]), pack_f16(s[0][2], s[0][3]),
@@ -336,10 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int w = 0; w < kWords; ++w) {
                     const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
                     const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                    mma_f16(O[4 * w], a, e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(y0));
-                    mma_f16(O[4 * w + 1], a, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(y0 >> 16));
-                    mma_f16(O[4 * w + 2], a, e4m3x2_to_f16x2(x1), e4m3x2_to_f16x2(y1));
-                    mma_f16(O[4 * w + 3], a, e4m3x2_to_f16x2(x1 >> 16), e4m3x2_to_f16x2(y1 >> 16));
+                    uint32_t b[8];
+                    e4m3x4_to_f16x4(x0, b[0], b[2]);
+                    e4m3x4_to_f16x4(y0, b[1], b[3]);
+                    e4m3x4_to_f16x4(x1, b[4], b[6]);
+                    e4m3x4_to_f16x4(y1, b[5], b[7]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_f16(O[4 * w + i], a, b[2 * i], b[2 * i + 1]);
                 }
                 if (poison) {
                     for (int t = 0; t < 16 && tok0 + t < seen_most; ++t) {
@@ -401,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             consumers_sync();
         }
 
-        const bool whole = seg.first_cta == seg.last_cta;
-        if (warp == 0 && whole && !bad_pages) {
+        if (warp == 0 && seg.whole && !bad_pages) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = r + 8 * i;
@@ -422,9 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.lse && j == 0) p.lse[at] = log_sum(M, L);
             }
         }
-        if (!whole) {
+        if (!seg.whole) {
             // ---- a part of a unit: to the workspace; the last CTA to come joins all parts
-            const int part_slot = 2 * blockIdx.x + (int(blockIdx.x) == seg.first_cta ? 1 : 0);
+            const int first_cta = line.first_cta(seg), last_cta = line.last_cta(seg);
+            const int part_slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
             if (warp == 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -442,17 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) {
-                    const int last = seg.last_cta - seg.first_cta;
-                    const bool mine = atomicAdd(&p.tickets[seg.first_cta], 1) == last;
-                    if (mine) p.tickets[seg.first_cta] = 0;
+                    const int last = last_cta - first_cta;
+                    const bool mine = atomicAdd(&p.tickets[first_cta], 1) == last;
+                    if (mine) p.tickets[first_cta] = 0;
                     __threadfence();
                     misc.ticket = mine;
                 }
             }
             consumers_sync();
             if (misc.ticket && !bad_pages) {
-                const int parts = seg.last_cta - seg.first_cta + 1;
-                auto slot_of = [&](int i) { return 2 * (seg.first_cta + i) + (i == 0); };
+                const int parts = last_cta - first_cta + 1;
+                auto slot_of = [&](int i) { return 2 * (first_cta + i) + (i == 0); };
                 float *weight = reinterpret_cast<float *>(smem + S::off_join);  // [16][parts]
                 for (int row = warp; row < seg.rows; row += kWarps) {
                     float M = kNone;
