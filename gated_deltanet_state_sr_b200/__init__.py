@@ -330,14 +330,15 @@ _lrb = _sig("sr_linrec_backward", _i32, ctypes.POINTER(LinrecGradArgs), _vp, cty
 
 def _want(t, name, dtypes, shape, device):
     """Checks an optional or required tensor of a call: a contiguous CUDA tensor on `device`."""
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _on_device(device, stream, body):
@@ -348,23 +349,35 @@ def _on_device(device, stream, body):
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
-            return body(ctypes.c_void_p(stream.cuda_stream))
+            return body(stream.cuda_stream)
     if torch.cuda.current_device() == device.index:
-        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        return body(_raw_stream(device.index))
     with torch.cuda.device(device):
-        return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        return body(_raw_stream(device.index))
 
 
-def _workspace_for(query, call, args, ws, device):
-    """The workspace of a call: the caller's, or a new one.  A query of 0 means that the arguments are refused."""
-    need = query(ctypes.byref(args))
-    if need == 0:
-        _check(call(ctypes.byref(args), None, 0, None))
-    if ws is None:
-        return workspace(need, device)
-    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+def _raw_stream(index):
+    """The current stream of a device (torch's own call for it where there is one: a third of a step's host time else)."""
+    torch = _torch()
+    quick = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return quick(index) if quick else torch.cuda.current_stream(index).cuda_stream
+
+
+_SPARE = {}
+
+
+def _workspace_for(need, ws, device):
+    """(address, bytes) of a call's workspace, and what keeps it alive: the caller's tensor, or a new one of `need` bytes."""
+    if ws is None and need <= 256:
+        # nobody reads the status word of a call without a workspace: one for all such calls of a device
+        ws = _SPARE.get(device.index)
+        if ws is None:
+            ws = _SPARE[device.index] = workspace(256, device)
+    elif ws is None:
+        ws = workspace(need, device)
+    elif not ws.is_cuda or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous CUDA tensor on {device}")
-    return ws
+    return ws.data_ptr(), _bytes(ws), ws
 
 
 def _bytes(t):
@@ -381,10 +394,11 @@ def _packed(t, name, cu_seqlens):
     torch = _torch()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    n, dev = cu_seqlens.numel() - 1, t.device
+    if cu_seqlens.dim() != 1 or n < 0:
         raise ValueError("cu_seqlens must have n_seqs + 1 entries")
-    _want(cu_seqlens, "cu_seqlens", (torch.int32,), tuple(cu_seqlens.shape), t.device)
-    return t.device, cu_seqlens.numel() - 1
+    _want(cu_seqlens, "cu_seqlens", (torch.int32,), (n + 1,), dev)
+    return dev, n
 
 
 def linrec_replay(x, g, cu_seqlens, *, max_seqlen, h0=None, want_y=True, y=None, s_out=None, ws=None, stream=None):
@@ -414,8 +428,8 @@ def linrec_replay(x, g, cu_seqlens, *, max_seqlen, h0=None, want_y=True, y=None,
         args = LinrecArgs(_addr(x), _addr(g), cu_seqlens.data_ptr(), None if h0 is None else _addr(h0),
                           None if yy is None else _addr(yy), _addr(s), SR_FP32 if x.dtype == torch.float32 else SR_BF16,
                           SR_FP32 if g.dtype == torch.float32 else SR_BF16, n, T, max_seqlen, D)
-        w = _workspace_for(_lr_ws, _lr, args, ws, dev)
-        _check(_lr(ctypes.byref(args), w.data_ptr(), _bytes(w), st))
+        at, size, keep = _workspace_for(256, ws, dev)
+        _check(_lr(ctypes.byref(args), at, size, st))
         return yy, s
 
     return _on_device(dev, stream, body)
@@ -449,8 +463,8 @@ def linrec_backward(g, y, dy, cu_seqlens, *, max_seqlen, h0=None, ds=None, dx=No
                               None if ds is None else _addr(ds), _addr(gx), _addr(gg), _addr(gh),
                               SR_FP32 if y.dtype == torch.float32 else SR_BF16,
                               SR_FP32 if g.dtype == torch.float32 else SR_BF16, n, T, max_seqlen, D)
-        w = _workspace_for(_lrb_ws, _lrb, args, ws, dev)
-        _check(_lrb(ctypes.byref(args), w.data_ptr(), _bytes(w), st))
+        at, size, keep = _workspace_for(256, ws, dev)
+        _check(_lrb(ctypes.byref(args), at, size, st))
         return gx, gg, gh
 
     return _on_device(dev, stream, body)
@@ -567,8 +581,8 @@ def kv_append(k, v, cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale,
                          _addr(k_scale), _addr(v_scale), ks, vs, qs, os_ if q_out is not None else h_q * d, n, T,
                          max_seqlen, h_q, h_kv, d, page, pages, block_table.shape[1], 2 * half, int(interleaved), axes,
                          (_i32 * 3)(*sections))
-        w = _workspace_for(_kva_ws, _kva, a, ws, dev)
-        _check(_kva(ctypes.byref(a), w.data_ptr(), _bytes(w), st))
+        at, size, keep = _workspace_for(256, ws, dev)
+        _check(_kva(ctypes.byref(a), at, size, st))
         return out
 
     return _on_device(dev, stream, body)
@@ -621,8 +635,8 @@ def paged_attention(q, cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_sca
                                _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(out),
                                None if ll is None else _addr(ll), qs, n, T, max_seqlen, max_kvlen, h_q, h_kv, d, page,
                                pages, block_table.shape[1], float(scale))
-        w = _workspace_for(_att_ws, _att, a, ws, dev)
-        _check(_att(ctypes.byref(a), w.data_ptr(), _bytes(w), st))
+        at, size, keep = _workspace_for(_att_ws(ctypes.byref(a)) if ws is None else 0, ws, dev)
+        _check(_att(ctypes.byref(a), at, size, st))
         return out, ll
 
     return _on_device(dev, stream, body)

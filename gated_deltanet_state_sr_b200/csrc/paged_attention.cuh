@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_
 // by tile.  On the line tile r of a sequence has a length in closed form, about
 // the cached tokens that it sees times the group, and a constant for what a unit
 // costs beside its blocks:
-//     length(r) = START + (cached before the new tokens) group + (r + 1) ROWS,
+//     length(r) = (START + cached before the new tokens) group + (r + 1) ROWS,
 // so that the place of every tile follows from a sum.  Offset x of a tile is its
 // block floor(x blocks / length): a cut falls on the same block for the CTA that
 // ends there and the one that begins there.
@@ -94,7 +94,7 @@ template <int ROWS, int TOK, int START> struct Line {
     long long cur, end, total, at, per_head;  // at: where the current head's tiles begin
     int ctas, seq, bos, count, kv, tiles, head, tile;
 
-    __device__ __forceinline__ long long lead() const { return (long long)START + (long long)max(0, kv - count) * p->group; }
+    __device__ __forceinline__ long long lead() const { return (long long)(START + max(0, kv - count)) * p->group; }
     __device__ __forceinline__ long long tiles_length(int n) const { return n * lead() + (long long)ROWS * n * (n + 1) / 2; }
 
     // Sequence n; the length of one of its heads, 0 where its entries are out of range (or it has no rows).

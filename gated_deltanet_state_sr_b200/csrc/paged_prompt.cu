@@ -36,7 +36,7 @@ constexpr int kThreads = 512;
 constexpr int kTok = 128;       // cached tokens per tile
 constexpr int kHalf = 64;       // tokens per stage of values
 constexpr int kMinBlocks = 2;   // least tiles worth a CTA of their own
-constexpr int kUnitStart = 512; // what a unit costs beside its tokens, in tokens of one head
+constexpr int kUnitStart = 512; // what a unit costs beside its tiles, in tokens
 // 256 x 160 + 128 x 96 + 128 x 96 = 512 x 128, what the block is launched with.
 constexpr int kSoftmaxRegs = 160, kConvertRegs = 96, kIssueRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= 512 * 128, "the split draws on the launch's");
@@ -237,47 +237,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (items == 0 && unit && !wait(misc.o_free, unit - 1)) break;
                 kt += tiles, vt += 2 * tiles, w += items;
             }
-        } else if (warp == 13) {
-            // ---- keys: a page (64 rows of it at most) per lane; pages behind the sequence's end are not read
-            int kt = 0;
+        } else if (warp == 13 || warp == 14) {
+            // ---- loads: keys, and values by a warp of their own (a wait for either ring would hold up the other).  A
+            // page (64 rows of it at most) per lane; pages behind the sequence's end are not read.
+            const bool keys = warp == 13;
+            const CUtensorMap *map = keys ? &kmap : &vmap;
+            uint64_t *full = keys ? misc.k_full : misc.raw_full, *empty = keys ? misc.k_empty : misc.raw_empty;
+            const int tokens = keys ? kTok : kHalf, stages = keys ? S::kKStages : S::kRawStages;
+            uint8_t *ring = smem + (keys ? S::off_k : S::off_raw);
             const int rows = min(p.page, 64);
+            int st = 0, round = 0;  // the stage, and how often the ring was filled before
             while (line.next(seg))
-                for (int b = seg.b0; b < seg.b1; ++b, ++kt) {
-                    const int st = kt % S::kKStages, at = b * kTok + lane * rows;
-                    const int pieces = (min(kTok, seg.kv - b * kTok) + rows - 1) / rows;
+#pragma unroll 1
+                for (int t0 = seg.b0 * kTok; t0 < seg.b1 * kTok; t0 += tokens) {
+                    const int pieces = (min(tokens, max(0, seg.kv - t0)) + rows - 1) / rows, at = t0 + lane * rows;
                     int y = 0, ok = 1;
-                    if (lane < pieces) y = (page_at(p, seg.seq, at) * p.h_kv + seg.head) * p.page + at % p.page;
+                    if (lane < pieces) y = (page_at(p, seg.seq, at) * p.h_kv + seg.head) * p.page + (at & (p.page - 1));
                     if (lane == 0) {
-                        ok = kt < S::kKStages || wait(misc.k_empty[st], kt / S::kKStages - 1);
-                        if (ok) tc::mbar_arrive_expect_tx(&misc.k_full[st], pieces * rows * D);
+                        ok = round == 0 || wait(empty[st], round - 1);
+                        if (ok) tc::mbar_arrive_expect_tx(&full[st], pieces * rows * D);
                     }
                     if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
                     if (lane < pieces)
 #pragma unroll
                         for (int x = 0; x < S::kSubs; ++x)
-                            tc::tma_load_2d(smem + S::off_k + st * S::kK + x * kTok * 128 + lane * rows * S::kSub, &kmap,
-                                            &misc.k_full[st], x * 128, y);
-                }
-        } else if (warp == 14) {
-            // ---- values, a warp of their own: a wait for either ring would hold up the other
-            int vt = 0;
-            const int rows = min(p.page, 64);
-            while (line.next(seg))
-                for (int t0 = seg.b0 * kTok; t0 < seg.b1 * kTok; t0 += kHalf, ++vt) {
-                    const int st = vt % S::kRawStages, at = t0 + lane * rows;
-                    const int pieces = (min(kHalf, max(0, seg.kv - t0)) + rows - 1) / rows;
-                    int y = 0, ok = 1;
-                    if (lane < pieces) y = (page_at(p, seg.seq, at) * p.h_kv + seg.head) * p.page + at % p.page;
-                    if (lane == 0) {
-                        ok = vt < S::kRawStages || wait(misc.raw_empty[st], vt / S::kRawStages - 1);
-                        if (ok) tc::mbar_arrive_expect_tx(&misc.raw_full[st], pieces * rows * D);
-                    }
-                    if (!__shfl_sync(0xffffffffu, ok, 0)) goto done;
-                    if (lane < pieces)
-#pragma unroll
-                        for (int x = 0; x < S::kSubs; ++x)
-                            tc::tma_load_2d(smem + S::off_raw + st * S::kRaw + x * kHalf * 128 + lane * rows * S::kSub, &vmap,
-                                            &misc.raw_full[st], x * 128, y);
+                            tc::tma_load_2d(ring + st * tokens * D + x * tokens * 128 + lane * rows * S::kSub, map, &full[st],
+                                            x * 128, y);
+                    if (++st == stages) st = 0, ++round;
                 }
         }
     } else if (warp >= 8) {
@@ -373,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (checked != seg.seq) {
                 bool bad = false;
                 const int pages = (seg.kv + p.page - 1) >> p.page_shift;
+#pragma unroll 1
                 for (int i = kSplit ? threadIdx.x : row; i < pages; i += bar_count) {
                     const int page = p.table[(long long)seg.seq * p.max_pages + i];
                     bad |= page < 0 || page >= p.n_pages;
@@ -631,7 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int parts = last_cta - first_cta + 1;
                 auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
                 float M = kNone, L = 0.f;
+#pragma unroll 1
                 for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
+#pragma unroll 1
                 for (int i = 0; i < parts; ++i) {
                     const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
                     L = fmaf(ml.y, exp2f(ml.x - M), L);
@@ -640,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
                     float4 sum[8] = {};
+#pragma unroll 1
                     for (int i = 0; i < parts; ++i) {
                         const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
                         const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;

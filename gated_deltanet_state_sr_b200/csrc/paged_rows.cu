@@ -42,7 +42,7 @@ constexpr int kLaunchRegs = 168, kLoadRegs = 40, kMathRegs = 232;
 static_assert(128 * kLoadRegs + 32 * kWarps * kMathRegs <= kThreads * kLaunchRegs, "the split draws on the launch's registers");
 constexpr int kTok = 64;               // tokens per stage: 4 warps of 16
 constexpr int kMinBlocks = 2;          // least blocks worth a CTA of their own
-constexpr int kUnitStart = 64;         // what a unit costs beside its tokens, in tokens of one head
+constexpr int kUnitStart = 256;         // what a unit costs beside its blocks, in tokens
 
 // Join barrier of the eight consumer warps.
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
