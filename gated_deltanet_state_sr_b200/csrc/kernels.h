@@ -49,6 +49,8 @@ cudaError_t gdn_tc_batch(const GdnBatch &b, int n_groups, int n_seqs, int d, boo
 bool make_map_bf16(CUtensorMap *m, const void *base, int rows, int cols, int pitch, int box_cols, int box_rows);
 // bytes [rows, cols] (row pitch `pitch` bytes), 128-byte swizzled boxes of box_rows x box_cols.
 bool make_map_u8(CUtensorMap *m, const void *base, int rows, int cols, int pitch, int box_cols, int box_rows);
+// fp32 or bf16 (esize 4 or 2) rows [rows, cols], unswizzled boxes; a row's bytes and the base are multiples of 16.
+bool make_map_rows(CUtensorMap *m, const void *base, int esize, int rows, int cols, int box_cols, int box_rows);
 // e4m3 cache rows [rows, cols], boxes of box_rows x 128 bytes (128-byte swizzle), or x 64 where cols is 64 (64-byte).
 bool make_map_cache(CUtensorMap *m, const void *base, int rows, int cols, int box_rows);
 // fp32 [rows, cols] (row pitch `pitch` elements), unswizzled boxes of box_rows x box_cols.

@@ -12,6 +12,7 @@
 // Both are bound by memory: forward moves x, g in and y out, backward g, dy, y
 // in and dx, dg out, each once.
 #include "common.cuh"
+#include "kernels.h"
 #include "tc.cuh"
 
 namespace sr {
@@ -140,6 +141,86 @@ __global__ void __launch_bounds__(128) linrec_short(LinrecParams p) {
             if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = h[c];
 }
 
+// tc::mbar_wait for a barrier that other CTAs of the cluster complete.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t phase) {
+    if (tc::mbar_try_wait_cluster(bar, phase)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t i = 1; !tc::mbar_try_wait_cluster(bar, phase); ++i)
+        if (i % 32 == 0 && tc::globaltimer_ns() - t0 > tc::kWaitLimitNs) return false;
+    return true;
+}
+
+// The state that enters a warp's tokens, h, and the one that leaves the wave, carry: every warp folds its tokens'
+// map, the CTA its warps', the cluster its CTAs', in token order each.  after_sync runs in every thread once all of
+// the CTA's have folded their tokens.
+template <int VEC, bool BWD, typename F>
+__device__ __forceinline__ void exchange(const float (&a)[kSteps][VEC], const float (&b)[kSteps][VEC], float (&carry)[VEC],
+                                         float (&h)[VEC], float2 (*warp_map)[32 * VEC], float2 (*cta_map)[32 * VEC],
+                                         uint64_t *arrived, int phase, int C, int rank, uint32_t *status, F after_sync) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+        float A = 1.f, B = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            A *= a[i][c];
+            B = step<BWD>(a[i][c], b[i][c], B);
+        }
+        warp_map[warp][lane * VEC + c] = make_float2(A, B);
+    }
+    __syncthreads();
+    after_sync();
+    if (C > 1) {
+        if (threadIdx.x < 32 * VEC) {
+            float A = 1.f, B = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 m = warp_map[w][threadIdx.x];
+                A *= m.x;
+                B = fmaf(m.x, B, m.y);
+            }
+            // The maps travel with their own arrival: a barrier of the cluster would also wait for the rows stored before
+            // it, seven microseconds a wave under load.  A CTA sends its next-but-one map, into the same place, only
+            // after it has every CTA's next one, and those were sent after this place was read.
+            const uint32_t mine = tc::smem_u32(&cta_map[rank][threadIdx.x]), bar = tc::smem_u32(arrived);
+            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(arrived, C * 32 * VEC * sizeof(float2));
+            for (int r = 0; r < C; ++r)
+                asm volatile(
+                    "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
+                        tc::mapa_shared(mine, r)),
+                    "f"(A), "f"(B), "r"(tc::mapa_shared(bar, r))
+                    : "memory");
+        }
+        if (!wait_cluster(arrived, phase)) atomicOr(status, SR_DEV_TIMEOUT);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h[c] = carry[c];
+        for (int r = 0; r < C; ++r)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                if (r == rank) h[c] = carry[c];
+                const float2 m = cta_map[r][lane * VEC + c];
+                carry[c] = fmaf(m.x, carry[c], m.y);
+            }
+#pragma unroll
+        for (int w = 0; w < kWarps - 1; ++w)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                const float2 m = warp_map[w][lane * VEC + c];
+                h[c] = w < warp ? fmaf(m.x, h[c], m.y) : h[c];
+            }
+    } else {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                const float2 m = warp_map[w][lane * VEC + c];
+                h[c] = w == warp ? carry[c] : h[c];
+                carry[c] = fmaf(m.x, carry[c], m.y);
+            }
+    }
+}
+
 // Long sequences.  A cluster of C CTAs walks one sequence of 32 VEC channels
 // in waves of C * kWarps * kSteps tokens; warp w of CTA r holds kSteps
 // consecutive tokens of the wave in registers, lane l the channels VEC l ...
@@ -155,13 +236,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) linrec_scan(LinrecParams p) {
     constexpr int kCols = 32 * VEC;
     __shared__ float2 warp_map[2][kWarps][kCols];
     __shared__ float2 cta_map[2][kMaxCluster][kCols];
+    __shared__ uint64_t arrived[2];
     __shared__ int scratch[kLongestFirstMax + 1];
     const int C = p.cluster, rank = C > 1 ? int(tc::cluster_ctarank()) : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int seq = longest_first(p.cu, p.n_seqs, blockIdx.y, scratch);
     int bos, eos;
     if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;  // the whole cluster alike
-    if (C > 1) tc::cluster_sync();  // every CTA's shared memory exists before the first remote write
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&arrived[i], 1);
+        tc::fence_mbar_init();
+    }
+    if (C > 1) tc::cluster_sync();  // every CTA's shared memory is there before the first remote write
     const int len = eos - bos;
     const int c0 = (blockIdx.x / C) * kCols + lane * VEC;
     const bool col = c0 < p.D;  // VEC divides D
@@ -180,101 +266,41 @@ __global__ void __launch_bounds__(kWarps * 32, 2) linrec_scan(LinrecParams p) {
     typename Vec<XT, VEC>::Raw rx[kSteps], ry[kSteps];
     const int seg = (rank * kWarps + warp) * kSteps;
     const int wave = C * kWarps * kSteps;
-    // token of step i in walking order; rows are loaded where they exist
+    // Token of step i in walking order.  Where there is none, zeros: exp(0) h + 0 leaves the state, and the arithmetic
+    // needs no branch, which would keep the steps from overlapping.
     auto fetch = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = base + seg + i;
-            if (col && r < len) {
-                const int t = BWD ? eos - 1 - r : bos + r;
-                const long long off = (long long)t * p.D + c0;
-                rg[i] = load_row<GT, VEC>(p.g, off, nel, p.status);
-                rx[i] = load_row<XT, VEC>(p.in, off, nel, p.status);
-                if (BWD && t > bos) ry[i] = load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status);
-            }
+            const int t = BWD ? eos - 1 - r : bos + r;
+            const long long off = (long long)t * p.D + c0;
+            const bool there = col && r < len;
+            rg[i] = typename Vec<GT, VEC>::Raw{};
+            rx[i] = ry[i] = typename Vec<XT, VEC>::Raw{};
+            if (there) rg[i] = load_row<GT, VEC>(p.g, off, nel, p.status);
+            if (there) rx[i] = load_row<XT, VEC>(p.in, off, nel, p.status);
+            if (BWD && there && t > bos) ry[i] = load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status);
         }
     };
     fetch(0);
-    int par = 0;
+    int par = 0, turn = 0;
     for (int base = 0; base < len; base += wave, par ^= 1) {
         float a[kSteps][VEC], b[kSteps][VEC], prev[kSteps][VEC];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const int r = base + seg + i;
-            if (col && r < len) {
-                float g[VEC];
-                Vec<GT, VEC>::get(rg[i], g);
-                Vec<XT, VEC>::get(rx[i], b[i]);
-                if (BWD) Vec<XT, VEC>::get(ry[i], prev[i]);
+            float g[VEC];
+            Vec<GT, VEC>::get(rg[i], g);
+            Vec<XT, VEC>::get(rx[i], b[i]);
+            if (BWD) Vec<XT, VEC>::get(ry[i], prev[i]);
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) {
-                    a[i][c] = decay(g[c]);
-                    if (BWD && r == len - 1) prev[i][c] = h0[c];
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) a[i][c] = 1.f, b[i][c] = 0.f, prev[i][c] = 0.f;
+            for (int c = 0; c < VEC; ++c) {
+                a[i][c] = decay(g[c]);
+                if (BWD) prev[i][c] = base + seg + i == len - 1 ? h0[c] : prev[i][c];
             }
         }
         if (base + wave < len) fetch(base + wave);
-        // this warp's map
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            float A = 1.f, B = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                A *= a[i][c];
-                B = step<BWD>(a[i][c], b[i][c], B);
-            }
-            warp_map[par][warp][lane * VEC + c] = make_float2(A, B);
-        }
-        __syncthreads();
         float h[VEC];
-        if (C > 1) {
-            if (threadIdx.x < kCols) {
-                float A = 1.f, B = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 m = warp_map[par][w][threadIdx.x];
-                    A *= m.x;
-                    B = fmaf(m.x, B, m.y);
-                }
-                const uint32_t mine = tc::smem_u32(&cta_map[par][rank][threadIdx.x]);
-                for (int r = 0; r < C; ++r)
-                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(tc::mapa_shared(mine, r)), "f"(A),
-                                 "f"(B)
-                                 : "memory");
-            }
-            tc::cluster_sync();
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                float v = carry[c];
-                h[c] = v;
-                for (int r = 0; r < C; ++r) {
-                    const float2 m = cta_map[par][r][lane * VEC + c];
-                    v = fmaf(m.x, v, m.y);
-                    if (r + 1 == rank) h[c] = v;
-                }
-                carry[c] = v;
-                for (int w = 0; w < warp; ++w) {
-                    const float2 m = warp_map[par][w][lane * VEC + c];
-                    h[c] = fmaf(m.x, h[c], m.y);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                float v = carry[c];
-                h[c] = v;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 m = warp_map[par][w][lane * VEC + c];
-                    v = fmaf(m.x, v, m.y);
-                    if (w + 1 == warp) h[c] = v;
-                }
-                carry[c] = v;
-            }
-        }
+        exchange<VEC, BWD>(a, b, carry, h, warp_map[par], cta_map[par], &arrived[par], (turn++ >> 1) & 1, C, rank, p.status, [] {});
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int r = base + seg + i;
@@ -300,8 +326,162 @@ __global__ void __launch_bounds__(kWarps * 32, 2) linrec_scan(LinrecParams p) {
             if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = carry[c];
 }
 
+// The same walk with the rows brought by TMA, 64 tokens by 64 channels at a time, into a ring of stages: what a memory
+// this fast needs in flight (200 KB an SM here) is more than registers hold.  For rows whose size is a multiple of 16
+// bytes, at an address that is.
+template <typename XT, typename GT, bool BWD> struct TmaShape {
+    static constexpr int kTok = kWarps * kSteps, kCols = 64;
+    static constexpr int kX = kTok * kCols * int(sizeof(XT)), kG = kTok * kCols * int(sizeof(GT));
+    static constexpr int kStage = kG + (BWD ? 2 : 1) * kX;
+    static constexpr int kStages = kStage > 40 * 1024 ? 2 : 3;
+    static constexpr int kMaps = 2 * (kWarps + kMaxCluster) * kCols * int(sizeof(float2));
+    static constexpr int bytes = kStages * kStage + kMaps + 64;
+    // Two CTAs of an SM (228 KB, of which each takes 1 KB more) hide each other's waits.
+    static constexpr int kPerSm = 2;
+    static_assert(kPerSm * (bytes + 1024) <= 228 * 1024, "two CTAs of an SM");
+};
+
+template <typename XT, typename GT, bool BWD>
+__global__ void __launch_bounds__(kWarps * 32, TmaShape<XT, GT, BWD>::kPerSm)
+    linrec_tma(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap gmap,
+               const __grid_constant__ CUtensorMap ymap, const __grid_constant__ LinrecParams p) {
+    using S = TmaShape<XT, GT, BWD>;
+    constexpr int VEC = 2, kCols = S::kCols;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float2(*warp_map)[kWarps][kCols] = reinterpret_cast<float2(*)[kWarps][kCols]>(smem + S::kStages * S::kStage);
+    float2(*cta_map)[kMaxCluster][kCols] = reinterpret_cast<float2(*)[kMaxCluster][kCols]>(warp_map + 2);
+    uint64_t *full = reinterpret_cast<uint64_t *>(cta_map + 2), *arrived = full + S::kStages;
+    static_assert(sizeof(float2) * 2 * kWarps * kCols >= (kLongestFirstMax + 1) * sizeof(int), "the order's scratch");
+    int *scratch = reinterpret_cast<int *>(warp_map);
+    const int C = p.cluster, rank = C > 1 ? int(tc::cluster_ctarank()) : 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seq = p.n_seqs > 1 ? longest_first(p.cu, p.n_seqs, blockIdx.y, scratch) : 0;
+    int bos, eos;
+    if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;  // the whole cluster alike
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) tc::mbar_init(&full[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&arrived[i], 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    if (C > 1) tc::cluster_sync();  // every CTA's shared memory is there before the first remote write
+    const int len = eos - bos, wave = C * S::kTok, seg = rank * S::kTok;
+    const int col0 = (blockIdx.x / C) * kCols, c0 = col0 + lane * VEC;
+    const bool col = c0 < p.D;
+    const long long nel = (long long)p.total * p.D, nst = (long long)p.n_seqs * p.D;
+    const long long soff = (long long)seq * p.D + c0;
+
+    // rows of a wave: forward from its first token on, backward up to it, so that row 0 is the last in walking order
+    auto fetch = [&](int base, int st) {
+        const int r = base + seg;
+        if (r >= len) return;
+        uint8_t *to = smem + st * S::kStage;
+        const int row = BWD ? eos - r - S::kTok : bos + r;
+        tc::mbar_arrive_expect_tx(&full[st], S::kStage);
+        tc::tma_load_2d(to, &gmap, &full[st], col0, row);
+        tc::tma_load_2d(to + S::kG, &xmap, &full[st], col0, row);
+        if (BWD) tc::tma_load_2d(to + S::kG + S::kX, &ymap, &full[st], col0, row - 1);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < S::kStages; ++i)
+            if (i * wave < len) fetch(i * wave, i);
+
+    float carry[VEC] = {}, h0[VEC] = {};
+    if (col) {
+        load_state<VEC>(BWD ? p.ds : p.h0, soff, nst, p.status, carry);
+        if (BWD) load_state<VEC>(p.h0, soff, nst, p.status, h0);
+    }
+    bool alive = true;
+    int par = 0, turn = 0, st = 0, round = 0;
+    for (int base = 0; base < len; base += wave, par ^= 1) {
+        const int r0 = base + seg + warp * kSteps;
+        if (base + seg < len && alive && !tc::mbar_wait(&full[st], round & 1)) {
+            atomicOr(p.status, SR_DEV_TIMEOUT);
+            alive = false;  // the cluster's barriers are still met
+        }
+        float a[kSteps][VEC], b[kSteps][VEC], prev[kSteps][VEC];
+        const uint8_t *from = smem + st * S::kStage;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int at = (BWD ? S::kTok - 1 - (warp * kSteps + i) : warp * kSteps + i) * kCols + lane * VEC;
+            const bool there = r0 + i < len;
+            float g[VEC];
+            Vec<GT, VEC>::get(*reinterpret_cast<const typename Vec<GT, VEC>::Raw *>(from + at * sizeof(GT)), g);
+            Vec<XT, VEC>::get(*reinterpret_cast<const typename Vec<XT, VEC>::Raw *>(from + S::kG + at * sizeof(XT)), b[i]);
+            if (BWD)
+                Vec<XT, VEC>::get(*reinterpret_cast<const typename Vec<XT, VEC>::Raw *>(from + S::kG + S::kX + at * sizeof(XT)),
+                                  prev[i]);
+            // a row behind the sequence leaves the state: exp(0) h + 0
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                a[i][c] = decay(there ? g[c] : 0.f);
+                b[i][c] = there ? b[i][c] : 0.f;
+                if (BWD) prev[i][c] = r0 + i == len - 1 ? h0[c] : prev[i][c];
+            }
+        }
+        float h[VEC];
+        exchange<VEC, BWD>(a, b, carry, h, warp_map[par], cta_map[par], &arrived[par], (turn++ >> 1) & 1, C, rank, p.status, [&] {
+            // every thread has read the stage
+            if (threadIdx.x == 0 && base + S::kStages * wave < len && alive) fetch(base + S::kStages * wave, st);
+        });
+        if (++st == S::kStages) st = 0, ++round;
+        const int t0 = BWD ? eos - 1 - r0 : bos + r0;
+        const long long off0 = (long long)t0 * p.D + c0, pitch = BWD ? -(long long)p.D : (long long)p.D;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const bool there = col && r0 + i < len;
+            float o[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                if (BWD) o[c] = b[i][c] + h[c];
+                h[c] = step<BWD>(a[i][c], b[i][c], h[c]);
+                if (!BWD) o[c] = h[c];
+                if (BWD) prev[i][c] *= h[c];
+            }
+            if (BWD && there) store_row<GT, VEC>(p.dg, off0 + i * pitch, nel, p.status, prev[i]);
+            if (p.out && there) store_row<XT, VEC>(p.out, off0 + i * pitch, nel, p.status, o);
+        }
+    }
+    if (p.last && col && rank == 0 && warp == 0)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = carry[c];
+}
+
 // A sequence of at most this many tokens is walked by one thread per channel pair.
 constexpr int kShortLen = 8;
+
+// A sequence's column block is spread over as many CTAs as the GPU holds at once, while each still has a wave of tokens
+// of its own: a cluster that has to wait for room would start when the others are done.
+template <typename K> int cluster_size(K kernel, cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, long long units, int max_len) {
+    for (int C = kMaxCluster; C > 1; --C) {
+        if ((C - 1) * kWarps * kSteps >= max_len) continue;
+        at->val.clusterDim.x = C;
+        cfg.gridDim.x = C;  // what the query looks at is the cluster
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) == cudaSuccess && fit >= units) return C;
+    }
+    (void)cudaGetLastError();
+    return 1;
+}
+
+void set_up(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, size_t smem, cudaStream_t st) {
+    cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at->id = cudaLaunchAttributeClusterDimension;
+    at->val.clusterDim.x = at->val.clusterDim.y = at->val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+}
+
+template <typename K> void set_grid(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, K kernel, LinrecParams &p, int blocks) {
+    p.cluster = cluster_size(kernel, cfg, at, (long long)blocks * p.n_seqs, p.max_len);
+    at->val.clusterDim.x = p.cluster;
+    cfg.gridDim = dim3(blocks * p.cluster, p.n_seqs);
+}
 
 template <typename XT, typename GT, int VEC, bool BWD>
 cudaError_t launch(LinrecParams p, cudaStream_t st) {
@@ -310,37 +490,50 @@ cudaError_t launch(LinrecParams p, cudaStream_t st) {
         linrec_short<XT, GT, VEC, BWD><<<dim3((p.D + per - 1) / per, p.n_seqs), 128, 0, st>>>(p);
         return cudaGetLastError();
     }
-    const int blocks = (p.D + 32 * VEC - 1) / (32 * VEC);
-    // A sequence's column block is spread over as many CTAs as fill the GPU
-    // (two per SM), while each still has a full wave of tokens.
-    int C = 1;
-    while (C < kMaxCluster && (long long)blocks * p.n_seqs * C < 2 * 148 && C * kWarps * kSteps < p.max_len) C *= 2;
-    p.cluster = C;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks * C, p.n_seqs);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = st;
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    set_up(cfg, at, 0, st);
+    set_grid(cfg, at, linrec_scan<XT, GT, VEC, BWD>, p, (p.D + 32 * VEC - 1) / (32 * VEC));
     return cudaLaunchKernelEx(&cfg, linrec_scan<XT, GT, VEC, BWD>, p);
+}
+
+template <typename XT, typename GT, bool BWD>
+cudaError_t launch_tma(LinrecParams p, cudaStream_t st) {
+    using S = TmaShape<XT, GT, BWD>;
+    CUtensorMap xm, gm, ym{};
+    if (!make_map_rows(&xm, p.in, sizeof(XT), p.total, p.D, S::kCols, S::kTok) ||
+        !make_map_rows(&gm, p.g, sizeof(GT), p.total, p.D, S::kCols, S::kTok) ||
+        (BWD && !make_map_rows(&ym, p.y_in, sizeof(XT), p.total, p.D, S::kCols, S::kTok)))
+        return cudaErrorInvalidValue;
+    auto kernel = linrec_tma<XT, GT, BWD>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at[1];
+    set_up(cfg, at, S::bytes, st);
+    set_grid(cfg, at, kernel, p, (p.D + S::kCols - 1) / S::kCols);
+    return cudaLaunchKernelEx(&cfg, kernel, xm, gm, ym, p);
+}
+
+template <typename XT, typename GT, bool BWD>
+cudaError_t pick(const LinrecParams &p, cudaStream_t st) {
+    // Two channels per thread where every row's pairs are aligned; rows by TMA where they are multiples of 16 bytes.
+    auto rows = [&](const void *q, size_t element, size_t align) {
+        return !q || (aligned(q, align) && size_t(p.D) * element % align == 0);
+    };
+    const bool two = rows(p.in, sizeof(XT), 2 * sizeof(XT)) && rows(p.g, sizeof(GT), 2 * sizeof(GT)) &&
+                     rows(p.y_in, sizeof(XT), 2 * sizeof(XT)) && rows(p.out, sizeof(XT), 2 * sizeof(XT)) &&
+                     rows(p.dg, sizeof(GT), 2 * sizeof(GT));
+    if (!two) return launch<XT, GT, 1, BWD>(p, st);
+    if (p.max_len > kShortLen && rows(p.in, sizeof(XT), 16) && rows(p.g, sizeof(GT), 16) && rows(p.y_in, sizeof(XT), 16))
+        return launch_tma<XT, GT, BWD>(p, st);
+    return launch<XT, GT, 2, BWD>(p, st);
 }
 
 template <bool BWD>
 cudaError_t dispatch(const LinrecParams &p, int dtype, int g_dtype, cudaStream_t st) {
-    // Two channels per thread where every row's pairs are aligned.
-    auto pairs = [&](const void *q, int type) { return !q || aligned(q, type == SR_BF16 ? 4 : 8); };
-    const bool two = p.D % 2 == 0 && pairs(p.in, dtype) && pairs(p.g, g_dtype) && pairs(p.y_in, dtype) &&
-                     pairs(p.out, dtype) && pairs(p.dg, g_dtype);
-    if (dtype == SR_FP32)
-        return two ? launch<float, float, 2, BWD>(p, st) : launch<float, float, 1, BWD>(p, st);
-    if (g_dtype == SR_FP32)
-        return two ? launch<__nv_bfloat16, float, 2, BWD>(p, st) : launch<__nv_bfloat16, float, 1, BWD>(p, st);
-    return two ? launch<__nv_bfloat16, __nv_bfloat16, 2, BWD>(p, st)
-               : launch<__nv_bfloat16, __nv_bfloat16, 1, BWD>(p, st);
+    if (dtype == SR_FP32) return pick<float, float, BWD>(p, st);
+    return g_dtype == SR_FP32 ? pick<__nv_bfloat16, float, BWD>(p, st) : pick<__nv_bfloat16, __nv_bfloat16, BWD>(p, st);
 }
 
 // Bounds that keep a token's and a channel's index, a wave or block past the end included, in an int.
