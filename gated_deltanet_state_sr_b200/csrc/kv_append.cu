@@ -18,6 +18,8 @@
 // rotation itself.  A warp takes one head of the page: keys and values in two
 // passes over the bf16 rows, the first for the largest magnitude, the second
 // from the caches that the first filled.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace sr {
@@ -68,16 +70,18 @@ __device__ __forceinline__ void unpack(uint2 r, float *f) {
     f[3] = __uint_as_float(r.y & 0xffff0000u);
 }
 
-// f[0..3] at u.lo, f[4..7] at u.hi.
-__device__ __forceinline__ void rotate(float (&f)[8], const Unit &u, const float2 *cs, int interleaved) {
-    if (u.pair < 0) return;
+// f[0..3] at u.lo, f[4..7] at u.hi.  Lanes without pairs keep what they have by selection: a branch would keep the
+// tokens of a batch from overlapping, and a product with (1, 0) would spread what is not finite.
+template <bool INTER>
+__device__ __forceinline__ void rotate(float (&f)[8], const Unit &u, const float2 *cs) {
+    const float2 *at = cs + max(u.pair, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 c = cs[u.pair + j];
-        float &lo = interleaved ? f[2 * j] : f[j], &hi = interleaved ? f[2 * j + 1] : f[4 + j];
-        const float a = lo, b = hi;
-        lo = a * c.x - b * c.y;
-        hi = a * c.y + b * c.x;
+        const float2 c = at[j];
+        float &lo = INTER ? f[2 * j] : f[j], &hi = INTER ? f[2 * j + 1] : f[4 + j];
+        const float x = lo * c.x - hi * c.y, y = lo * c.y + hi * c.x;
+        lo = u.pair < 0 ? lo : x;
+        hi = u.pair < 0 ? hi : y;
     }
 }
 
@@ -86,10 +90,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int D>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
     constexpr int kLanes = D / 8;         // lanes per token
     constexpr int kAtOnce = 32 / kLanes;  // tokens per warp and step
+    constexpr int kBatch = 4;             // steps whose rows are loaded together
     extern __shared__ float2 table_cs[];  // [tokens of the page][half]
     const int seq = blockIdx.z;
     int bos, eos;
@@ -121,27 +126,43 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
     const int page = p.table[(long long)seq * p.max_pages + slot];
     const bool page_ok = page >= 0 && page < p.n_pages;
     if (!page_ok && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
-    const Unit u = unit_of<D>(lane % kLanes, p.half, p.interleaved);
+    const Unit u = unit_of<D>(lane % kLanes, p.half, INTER);
     const Unit plain{8 * (lane % kLanes), 8 * (lane % kLanes) + 4, -1};
     const int sub = lane / kLanes;
+    // Calls use(t, f) for every token t of this lane, f being its eight elements; with `turn`, rotated.
+    auto walk = [&](const __nv_bfloat16 *src, long long stride, const Unit &w, auto turn, auto use) {
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += kBatch * kAtOnce) {
+            uint2 in[kBatch][2];  // behind the last token: the last once more, to the same result
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int t = min(t0 + sub + i * kAtOnce, n - 1);
+                const __nv_bfloat16 *row = src + t * stride;
+                in[i][0] = *reinterpret_cast<const uint2 *>(row + w.lo);
+                in[i][1] = *reinterpret_cast<const uint2 *>(row + w.hi);
+            }
+            __syncwarp();  // in place, every copy of a row is read before the first is written
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int t = min(t0 + sub + i * kAtOnce, n - 1);
+                float f[8];
+                unpack(in[i][0], f);
+                unpack(in[i][1], f + 4);
+                if (turn) rotate<INTER>(f, w, table_cs + t * p.half);
+                use(t, f);
+            }
+        }
+    };
     const int heads = p.h_q + 2 * p.h_kv;
     for (int item = blockIdx.y * kWarps + warp; item < heads; item += p.groups * kWarps) {
         if (item >= 2 * p.h_kv) {  // a query head: rotated rows
-            if (!p.q) break;
             const int h = item - 2 * p.h_kv;
-            const __nv_bfloat16 *src = p.q + (long long)tok0 * p.q_stride + h * D;
             __nv_bfloat16 *dst = p.q_out + (long long)tok0 * p.q_out_stride + h * D;
-#pragma unroll 4
-            for (int t = sub; t < n; t += kAtOnce) {
-                float f[8];
-                const __nv_bfloat16 *row = src + t * p.q_stride;
-                unpack(*reinterpret_cast<const uint2 *>(row + u.lo), f);
-                unpack(*reinterpret_cast<const uint2 *>(row + u.hi), f + 4);
-                rotate(f, u, table_cs + t * p.half, p.interleaved);
+            walk(p.q + (long long)tok0 * p.q_stride + h * D, p.q_stride, u, std::true_type{}, [&](int t, const float(&f)[8]) {
                 __nv_bfloat16 *out = dst + t * p.q_out_stride;
                 *reinterpret_cast<uint2 *>(out + u.lo) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
                 *reinterpret_cast<uint2 *>(out + u.hi) = make_uint2(pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-            }
+            });
             continue;
         }
         if (!page_ok) continue;
@@ -153,23 +174,15 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
         const long long block = (long long)page * p.h_kv + h;
         uint8_t *cache = (key ? p.k_cache : p.v_cache) + block * p.page * D;
         float *scale = (key ? p.k_scale : p.v_scale) + block;
-        auto value = [&](int t, float (&f)[8]) {
-            const __nv_bfloat16 *row = src + t * stride;
-            unpack(*reinterpret_cast<const uint2 *>(row + w.lo), f);
-            unpack(*reinterpret_cast<const uint2 *>(row + w.hi), f + 4);
-            rotate(f, w, table_cs + t * p.half, p.interleaved);
-        };
         float top = 0.f;
-#pragma unroll 4
-        for (int t = sub; t < n; t += kAtOnce) {
-            float f[8];
-            value(t, f);
+        auto largest = [&](int, const float(&f)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float m = fabsf(f[j]);
-                if (m <= 3.402823466e38f) top = fmaxf(top, m);  // a value that is not finite has no part in the scale
+                top = fmaxf(top, m <= 3.402823466e38f ? m : 0.f);  // what is not finite has no part in the scale
             }
-        }
+        };
+        if (key) walk(src, stride, w, std::true_type{}, largest); else walk(src, stride, w, std::false_type{}, largest);
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const int old = from - slot * p.page;  // tokens that the page held before
@@ -192,37 +205,42 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
             }
         }
         const float inv = 1.f / kept;
-#pragma unroll 4
-        for (int t = sub; t < n; t += kAtOnce) {
-            float f[8];
-            value(t, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= inv;
+        auto store = [&](int t, const float(&f)[8]) {
             uint8_t *out = cache + (old + t) * D;
-            *reinterpret_cast<uint32_t *>(out + w.lo) = paged::to_e4m3x4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint32_t *>(out + w.hi) = paged::to_e4m3x4(f[4], f[5], f[6], f[7]);
-        }
+            *reinterpret_cast<uint32_t *>(out + w.lo) = paged::to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+            *reinterpret_cast<uint32_t *>(out + w.hi) = paged::to_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+        };
+        if (key) walk(src, stride, w, std::true_type{}, store); else walk(src, stride, w, std::false_type{}, store);
     }
 }
 
-template <int D>
+template <int D, bool INTER>
 cudaError_t launch(AppendParams p, cudaStream_t st) {
     const int slots = (p.max_len + p.page - 2) / p.page + 1;  // pages that max_len tokens can touch
     const int heads = (p.q ? p.h_q : 0) + 2 * p.h_kv;
     // The heads of a page are shared out over as many CTAs as give the GPU eight warps per scheduler; every share
     // repeats the page's cosines and sines, so no more than that.
-    const long long tiles = (long long)slots * p.n_seqs;
+    // pages that there can be: of the longest sequences, and of all tokens with a part page at both ends
+    const long long most_tiles = (long long)slots * p.n_seqs, full = p.total / p.page + 2ll * p.n_seqs;
+    const long long tiles = most_tiles < full ? most_tiles : full;
     const int most = (heads + kWarps - 1) / kWarps;
     const long long want = (4 * 148 + tiles - 1) / tiles;
     p.groups = int(want < most ? want : most);
-    const size_t smem = size_t(p.page < p.max_len ? p.page : p.max_len) * p.half * sizeof(float2);
+    // Four entries at least: lanes without pairs (all of them without a rotation) read the first four of a token's, and
+    // keep what they have.
+    const size_t entries = size_t(p.page < p.max_len ? p.page : p.max_len) * p.half;
+    const size_t smem = (entries > 4 ? entries : 4) * sizeof(float2);
     static_assert(128 * 128 * sizeof(float2) <= 227 * 1024, "the largest table fits");
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(append_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        cudaError_t e = cudaFuncSetAttribute(append_kernel<D, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    append_kernel<D><<<dim3(slots, p.groups, p.n_seqs), kWarps * 32, smem, st>>>(p);
+    append_kernel<D, INTER><<<dim3(slots, p.groups, p.n_seqs), kWarps * 32, smem, st>>>(p);
     return cudaGetLastError();
+}
+
+template <bool INTER> cudaError_t pick(const AppendParams &p, int d, cudaStream_t st) {
+    return d == 64 ? launch<64, INTER>(p, st) : d == 128 ? launch<128, INTER>(p, st) : launch<256, INTER>(p, st);
 }
 
 sr_status validate(const sr_kv_append_args *a) {
@@ -300,6 +318,6 @@ extern "C" sr_status sr_kv_append(const sr_kv_append_args *a, void *ws, size_t w
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st);
     if (e == cudaSuccess && p.n_seqs > 0 && p.max_len > 0)
-        e = a->head_dim == 64 ? launch<64>(p, st) : a->head_dim == 128 ? launch<128>(p, st) : launch<256>(p, st);
+        e = p.interleaved ? pick<true>(p, a->head_dim, st) : pick<false>(p, a->head_dim, st);
     return e == cudaSuccess ? SR_OK : cuda_error(e, "sr_kv_append");
 }
