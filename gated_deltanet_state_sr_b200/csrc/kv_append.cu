@@ -73,11 +73,14 @@ __device__ __forceinline__ void unpack(uint2 r, float *f) {
 // f[0..3] at u.lo, f[4..7] at u.hi.  Lanes without pairs keep what they have by selection: a branch would keep the
 // tokens of a batch from overlapping, and a product with (1, 0) would spread what is not finite.
 template <bool INTER>
-__device__ __forceinline__ void rotate(float (&f)[8], const Unit &u, const float2 *cs) {
-    const float2 *at = cs + max(u.pair, 0);
+__device__ __forceinline__ void rotate(float (&f)[8], const Unit &u, const float2 *cs, int half) {
+    // a token's cosines and sines: pairs 4u, 4u+1 of every u, then 4u+2, 4u+3, so that lanes read neighbouring 16 bytes
+    const float2 *at = cs + max(u.pair, 0) / 2;
+    const float4 one = *reinterpret_cast<const float4 *>(at), two = *reinterpret_cast<const float4 *>(at + half / 2);
+    const float2 cc[4] = {{one.x, one.y}, {one.z, one.w}, {two.x, two.y}, {two.z, two.w}};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 c = at[j];
+        const float2 c = cc[j];
         float &lo = INTER ? f[2 * j] : f[j], &hi = INTER ? f[2 * j + 1] : f[4 + j];
         const float x = lo * c.x - hi * c.y, y = lo * c.y + hi * c.x;
         lo = u.pair < 0 ? lo : x;
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
     constexpr int kLanes = D / 8;         // lanes per token
     constexpr int kAtOnce = 32 / kLanes;  // tokens per warp and step
     constexpr int kBatch = 4;             // steps whose rows are loaded together
-    extern __shared__ float2 table_cs[];  // [tokens of the page][half]
+    extern __shared__ __align__(16) float2 table_cs[];  // [tokens of the page][half], in rotate's order
     const int seq = blockIdx.z;
     int bos, eos;
     if (!seq_bounds(p.cu, seq, p.total, p.max_len, p.status, bos, eos)) return;
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
         const double turns = double(pos) * double(p.inv_freq[pair]) * kTurnsPerRadian;
         float s, c;
         sincospif(2.f * float(turns - rint(turns)), &s, &c);
-        table_cs[i] = make_float2(c, s);
+        table_cs[t * p.half + (pair & 2) / 2 * (p.half / 2) + pair / 4 * 2 + (pair & 1)] = make_float2(c, s);
     }
     __syncthreads();
 
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
                 float f[8];
                 unpack(in[i][0], f);
                 unpack(in[i][1], f + 4);
-                if (turn) rotate<INTER>(f, w, table_cs + t * p.half);
+                if (turn) rotate<INTER>(f, w, table_cs + t * p.half, p.half);
                 use(t, f);
             }
         }
@@ -225,7 +228,8 @@ cudaError_t launch(AppendParams p, cudaStream_t st) {
     const long long tiles = most_tiles < full ? most_tiles : full;
     const int most = (heads + kWarps - 1) / kWarps;
     const long long want = (4 * 148 + tiles - 1) / tiles;
-    p.groups = int(want < most ? want : most);
+    const int rounds = want < most ? int((most + want - 1) / want) : 1;  // heads of a warp, the same for all
+    p.groups = (most + rounds - 1) / rounds;
     // Four entries at least: lanes without pairs (all of them without a rotation) read the first four of a token's, and
     // keep what they have.
     const size_t entries = size_t(p.page < p.max_len ? p.page : p.max_len) * p.half;
