@@ -144,6 +144,19 @@ def test_many_requests(sr):
     check(sr, make(new, kv, 4, 2, 128, 64, seed=4))
 
 
+@pytest.mark.parametrize("d,h_q,h_kv", [(256, 16, 4), (256, 16, 1), (128, 32, 8), (128, 16, 1), (64, 8, 4), (64, 12, 1)], ids=str)
+def test_many_stages_in_flight(sr, d, h_q, h_kv):
+    """Long and short sequences after one another in a CTA, their loads overtaking each other, several times over."""
+    rng = np.random.default_rng(21)
+    c = make([1] * 40, rng.integers(1, 1500, 40).tolist(), h_q, h_kv, d, 64, seed=21)
+    ref = check(sr, c)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        flush.zero_()
+        o, lse = call(sr, c)
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
 def test_prompts(sr):
     check(sr, make([300, 1, 129], [300, 50, 400], 8, 2, 128, 64, seed=5))
     check(sr, make([200], [200], 4, 1, 256, 16, seed=6))
