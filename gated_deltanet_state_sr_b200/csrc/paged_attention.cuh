@@ -74,8 +74,9 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_
 // costs beside its blocks:
 //     length(r) = (START + cached before the new tokens) group + (r + 1) ROWS,
 // so that the place of every tile follows from a sum.  Offset x of a tile is its
-// block floor(x blocks / length): a cut falls on the same block for the CTA that
-// ends there and the one that begins there.
+// block floor((x - START group) / (TOK group)), within its blocks: a cut falls on
+// the same block for the CTA that ends there and the one that begins there.  A cut
+// in a tile's START is one at its beginning: nobody has a part without blocks.
 struct Segment {
     int seq, head, tile, rows;   // rows: of this tile
     int b0, b1;                  // this CTA's blocks of the unit
@@ -89,10 +90,20 @@ struct LinePlace {
     int seq;
 };
 
+// a / b of numbers that are not negative; 64-bit division is a long subroutine that these kernels' starts would wait for.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 template <int ROWS, int TOK, int START> struct Line {
     const AttnParams *p;
-    long long cur, end, total, at, per_head;  // at: where the current head's tiles begin
-    int ctas, seq, bos, count, kv, tiles, head, tile;
+    long long cur, end, at, per_head;  // at: where the current head's tiles begin
+    long long share;                   // the line's length divided by the CTAs, and
+    int rest, ctas;                    // what is left of that
+    int seq, bos, count, kv, tiles, head, tile;
+
+    // Where the part of CTA c begins: the rest is spread evenly.
+    __device__ __forceinline__ long long part(int c) const { return c * share + c * rest / ctas; }
 
     __device__ __forceinline__ long long lead() const { return (long long)(START + max(0, kv - count)) * p->group; }
     __device__ __forceinline__ long long tiles_length(int n) const { return n * lead() + (long long)ROWS * n * (n + 1) / 2; }
@@ -118,56 +129,82 @@ template <int ROWS, int TOK, int START> struct Line {
     template <int THREADS> __device__ bool start(const AttnParams &params, long long least, LinePlace &place) {
         p = &params;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        long long mine = 0;
-#pragma unroll 1
-        for (int n = threadIdx.x; n < p->n_seqs; n += THREADS) mine += load(n, blockIdx.x == 0) * p->h_kv;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) place.scan[warp] = mine;
-        __syncthreads();
-        total = 0;
-#pragma unroll 1
-        for (int w = 0; w < THREADS / 32; ++w) total += place.scan[w];
-        if (total == 0) return false;
-        ctas = int(min((long long)gridDim.x, (total + least - 1) / least));
-        if (int(blockIdx.x) >= ctas) return false;
-        cur = blockIdx.x * total / ctas;
-        end = (blockIdx.x + 1) * total / ctas;
-        // the sequence that holds `cur`: sums over THREADS sequences at a time
-        long long before = 0;
-        for (int n0 = 0; before <= cur; n0 += THREADS) {
-            const int n = n0 + threadIdx.x;
-            const long long c = n < p->n_seqs ? load(n, false) * p->h_kv : 0;
-            long long incl = c;
+        long long total = 0, from = 0, mine = 0;
+        if (p->n_seqs <= 32) {  // every warp for itself, a sequence a lane
+            mine = lane < p->n_seqs ? load(lane, blockIdx.x == 0 && warp == 0) * p->h_kv : 0;
+            total = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
+                const long long up = __shfl_up_sync(0xffffffffu, total, o);
+                if (lane >= o) total += up;
             }
-            __syncthreads();
-            if (lane == 31) place.scan[warp] = incl;
-            __syncthreads();
-            long long from = before + incl - c, chunk = 0;
+            from = total - mine;
+            total = __shfl_sync(0xffffffffu, total, 31);
+        } else {
 #pragma unroll 1
-            for (int w = 0; w < THREADS / 32; ++w) {
-                if (w < warp) from += place.scan[w];
-                chunk += place.scan[w];
-            }
-            if (c > 0 && cur >= from && cur < from + c) place.seq = n, place.at = from;
-            before += chunk;
+            for (int n = threadIdx.x; n < p->n_seqs; n += THREADS) total += load(n, blockIdx.x == 0) * p->h_kv;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) place.scan[warp] = total;
+            __syncthreads();
+            total = 0;
+#pragma unroll 1
+            for (int w = 0; w < THREADS / 32; ++w) total += place.scan[w];
         }
-        __syncthreads();
-        seq = place.seq;
+        if (total == 0) return false;
+        ctas = int(min((long long)gridDim.x, divide(total + least - 1, least)));
+        if (int(blockIdx.x) >= ctas) return false;
+        share = divide(total, ctas), rest = int(total - share * ctas);
+        cur = part(blockIdx.x), end = part(blockIdx.x + 1);
+        if (p->n_seqs <= 32) {
+            const bool here = mine > 0 && cur >= from && cur < from + mine;
+            seq = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            at = __shfl_sync(0xffffffffu, from, seq);
+        } else {
+            // the sequence that holds `cur`: sums over THREADS sequences at a time
+            long long before = 0;
+#pragma unroll 1
+            for (int n0 = 0; before <= cur; n0 += THREADS) {
+                const int n = n0 + threadIdx.x;
+                mine = n < p->n_seqs ? load(n, false) * p->h_kv : 0;
+                long long incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                __syncthreads();
+                if (lane == 31) place.scan[warp] = incl;
+                __syncthreads();
+                long long chunk = 0;
+                from = before + incl - mine;
+#pragma unroll 1
+                for (int w = 0; w < THREADS / 32; ++w) {
+                    if (w < warp) from += place.scan[w];
+                    chunk += place.scan[w];
+                }
+                if (mine > 0 && cur >= from && cur < from + mine) place.seq = n, place.at = from;
+                before += chunk;
+            }
+            __syncthreads();
+            seq = place.seq, at = place.at;
+        }
         per_head = load(seq, false);
-        head = int((cur - place.at) / per_head);
-        at = place.at + head * per_head;
+        head = int(divide(cur - at, per_head));
+        at += head * per_head;
         int lo = 0, hi = tiles - 1;  // the last tile that begins at or before cur
+#pragma unroll 1
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (tiles_length(mid) <= cur - at) lo = mid; else hi = mid - 1;
         }
         tile = lo;
         return true;
+    }
+
+    __device__ __forceinline__ int block_at(long long x, int blocks) const {
+        const long long y = x - (long long)START * p->group;
+        return y <= 0 ? 0 : min(blocks, int(uint32_t(y / TOK) / uint32_t(p->group)));
     }
 
     __device__ __forceinline__ bool next(Segment &s) {
@@ -179,10 +216,15 @@ template <int ROWS, int TOK, int START> struct Line {
         s.length = lead() + (long long)(tile + 1) * ROWS;
         const int seen = max(0, kv - count + (tile * ROWS + s.rows - 1) / p->group + 1);
         const int blocks = (seen + TOK - 1) / TOK;
-        const long long x0 = cur - s.first, x1 = min(s.length, end - s.first);
+        const long long start = (long long)START * p->group;
+        const long long x0 = cur - s.first <= start ? 0 : cur - s.first, x1 = min(s.length, end - s.first);
+        if (x1 <= start) {
+            cur = end;
+            return false;
+        }
         s.whole = x0 == 0 && x1 == s.length;
-        s.b0 = x0 == 0 ? 0 : int(x0 * blocks / s.length);
-        s.b1 = x1 == s.length ? blocks : int(x1 * blocks / s.length);
+        s.b0 = x0 == 0 ? 0 : block_at(x0, blocks);
+        s.b1 = x1 == s.length ? blocks : block_at(x1, blocks);
         cur = s.first + x1;
         if (x1 == s.length && ++tile == tiles) {
             tile = 0;
@@ -197,9 +239,15 @@ template <int ROWS, int TOK, int START> struct Line {
         return true;
     }
 
-    // CTAs that hold the first and the last of a unit's places
-    __device__ __forceinline__ int first_cta(const Segment &s) const { return int(((s.first + 1) * ctas - 1) / total); }
-    __device__ __forceinline__ int last_cta(const Segment &s) const { return int(((s.first + s.length) * ctas - 1) / total); }
+    // The CTA that holds place x of the line, and those that hold a unit's first and last.
+    __device__ __forceinline__ int cta_of(long long x) const {
+        int c = int(min((long long)(ctas - 1), divide(x, max(share, 1ll))));
+        while (part(c) > x) --c;
+        while (part(c + 1) <= x) ++c;
+        return c;
+    }
+    __device__ __forceinline__ int first_cta(const Segment &s) const { return cta_of(s.first + (long long)START * p->group); }
+    __device__ __forceinline__ int last_cta(const Segment &s) const { return cta_of(s.first + s.length - 1); }
 };
 
 // tc::mbar_wait in few instructions: these kernels have a dozen places that wait, and what they run has to stay in the
@@ -211,6 +259,14 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t phase) {
     for (uint32_t i = 1; !tc::mbar_try_wait(bar, phase); ++i)
         if (i % 32 == 0 && tc::globaltimer_ns() - t0 > tc::kWaitLimitNs) return false;
     return true;
+}
+
+// Counts a part as written: what this thread wrote, or saw written by threads it met at a barrier, is there for whoever
+// takes the last ticket.
+__device__ __forceinline__ int take_ticket(int *ticket) {
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n" : "=r"(before) : "l"(ticket) : "memory");
+    return before;
 }
 
 // Tokens that row r of a segment's tile sees.

@@ -604,13 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
-            __threadfence();
             named_sync(bar_id, bar_count);
             if (row == 0 && out0 == 0) {
                 int *ticket = &p.tickets[first_cta * NQ + q_tile];
-                const bool mine = atomicAdd(ticket, 1) == last_cta - first_cta;
+                const bool mine = take_ticket(ticket) == last_cta - first_cta;
                 if (mine) *ticket = 0;
-                __threadfence();
                 misc.ticket[q_tile] = mine;
             }
             named_sync(bar_id, bar_count);

@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kTok = 64;               // tokens per stage: 4 warps of 16
 constexpr int kMinBlocks = 2;          // least blocks worth a CTA of their own
-constexpr int kUnitStart = 256;        // what a unit costs beside its blocks, in tokens
+constexpr int kUnitStart = 512;        // what a unit costs beside its blocks, in tokens
 
 // Consumer warps by what a lane has to hold: D / 4 sums for every eight queries, D / 8 bytes of values, fragments.
 template <int D, int NT> struct RowsShape {
@@ -126,7 +126,9 @@ template <int D, int NT> struct RowsSmem {
     struct Misc {
         uint64_t full[kStages], empty[kStages];
         float2 scale[kStages][4];           // of keys and values, of each 16 tokens or more
-        float ml[2][Shape::kWarps][kRows];  // running max and sum of each warp's rows
+        float2 ml[Shape::kWarps][kRows];    // running max and sum of each warp's rows
+        float2 sum_ml[kRows];               // and of all
+        float weight[Shape::kWarps][kRows];
         float row_scale[kRows];             // factor of q . k of each row
         int row_seen[kRows];                // tokens each row may see
         float sums[kRows];
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
             for (int t = 0; t < D / 16; ++t) O[n][t][0] = O[n][t][1] = O[n][t][2] = O[n][t][3] = 0.f;
         }
         const int seen_most = misc.row_seen[seg.rows - 1], seen_least = misc.row_seen[0];
-        const int b1 = seg.b1;
+        const int b1 = seg.b1, turn0 = turn;
 
 #pragma unroll 1
         for (int b = seg.b0; b < b1; ++b) {
@@ -441,49 +443,60 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
             if (lane == 0) tc::mbar_arrive(&misc.empty[at]);
         }
 
-        // ---- join the warps: rows' largest m, then sums in a fixed order
+        // ---- join the warps that had blocks: rows' largest m, then sums in a fixed order
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-                if (r == 0) misc.ml[0][warp][8 * n + 2 * j + e] = m[n][e], misc.ml[1][warp][8 * n + 2 * j + e] = l[n][e];
+                if (r == 0) misc.ml[warp][8 * n + 2 * j + e] = make_float2(m[n][e], l[n][e]);
             }
+        consumers_sync<N>();
+        // a warp per row, a lane per warp's share of it
+        for (int row = warp; row < S::kRows; row += kWarps) {
+            float2 x = lane < kWarps ? misc.ml[lane][row] : make_float2(kNone, 0.f);
+            float M = x.x;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float f = exp2f(x.x - M);
+            float L = x.y * f;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (lane < kWarps) misc.weight[lane][row] = f;
+            if (lane == 0) misc.sum_ml[row] = make_float2(M, L);
+        }
         consumers_sync<N>();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * n + 2 * j + e;
-                float M = kNone, L = 0.f;
-#pragma unroll 1
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, misc.ml[0][w][row]);
-#pragma unroll 1
-                for (int w = 0; w < kWarps; ++w) L = fmaf(misc.ml[1][w][row], exp2f(misc.ml[0][w][row] - M), L);
-                const float f = exp2f(m[n][e] - M);
-                m[n][e] = M, l[n][e] = L;
+                const float f = misc.weight[warp][row];
+                m[n][e] = misc.sum_ml[row].x, l[n][e] = misc.sum_ml[row].y;
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) O[n][t][e] *= f, O[n][t][2 + e] *= f;
             }
+        // the groups in the order of their first blocks; those behind had none
+        const int order = ((warp >> 2) - turn0 + Shape::kGroups) % Shape::kGroups * 4 + (warp & 3);
         float4 *join = reinterpret_cast<float4 *>(smem + S::off_join);
 #pragma unroll 1
-        for (int left = kWarps; left > 1;) {
+        for (int left = min(kWarps, max(4 * (b1 - seg.b0), 1)); left > 1;) {
             const int k = min(S::kRegions, left / 2);  // the last k warps' sums go to the k before them
-            if (warp >= left - k && warp < left)
+            if (order >= left - k && order < left)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int t = 0; t < D / 16; ++t)
-                        join[(((warp - left + k) * NT + n) * (D / 16) + t) * 32 + lane] =
+                        join[(((order - left + k) * NT + n) * (D / 16) + t) * 32 + lane] =
                             make_float4(O[n][t][0], O[n][t][1], O[n][t][2], O[n][t][3]);
             consumers_sync<N>();
-            if (warp >= left - 2 * k && warp < left - k)
+            if (order >= left - 2 * k && order < left - k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int t = 0; t < D / 16; ++t) {
-                        const float4 x = join[(((warp - left + 2 * k) * NT + n) * (D / 16) + t) * 32 + lane];
+                        const float4 x = join[(((order - left + 2 * k) * NT + n) * (D / 16) + t) * 32 + lane];
                         O[n][t][0] += x.x, O[n][t][1] += x.y, O[n][t][2] += x.z, O[n][t][3] += x.w;
                     }
             consumers_sync<N>();
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
             const int g = seg.tile * S::kRows + row;
             return (long long)(seg.bos + g / p.group) * p.h_q + seg.head * p.group + g % p.group;
         };
-        if (warp == 0 && seg.whole && !bad_pages) {
+        if (order == 0 && seg.whole && !bad_pages) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
             // ---- a part of a unit: to the workspace; the last CTA to come joins all parts
             const int first_cta = misc.first_cta, last_cta = misc.last_cta;
             const int part_slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
-            if (warp == 0) {
+            if (order == 0) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -529,12 +542,10 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
                                 make_float4(O[n][t / 2][e], O[n][t / 2][2 + e], O[n][t / 2 + 1][e], O[n][t / 2 + 1][2 + e]);
                         if (r == 0) p.part_ml[part_slot * 16 + row] = make_float2(m[n][e], l[n][e]);
                     }
-                __threadfence();
                 __syncwarp();
                 if (lane == 0) {
-                    const bool mine = atomicAdd(&p.tickets[first_cta], 1) == last_cta - first_cta;
+                    const bool mine = take_ticket(&p.tickets[first_cta]) == last_cta - first_cta;
                     if (mine) p.tickets[first_cta] = 0;
-                    __threadfence();
                     misc.ticket = mine;
                 }
             }
@@ -545,15 +556,17 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
                 float *weight = reinterpret_cast<float *>(smem + S::off_join);  // [rows][parts]
 #pragma unroll 1
                 for (int row = warp; row < seg.rows; row += kWarps) {
-                    float M = kNone;
+                    float2 x = make_float2(kNone, 0.f);  // this lane's first part, loaded once
+                    if (lane < parts) x = __ldcg(&p.part_ml[slot_of(lane) * 16 + row]);
+                    float M = x.x;
 #pragma unroll 1
-                    for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + row]).x);
+                    for (int i = lane + 32; i < parts; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + row]).x);
 #pragma unroll
                     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
                     float L = 0.f;
 #pragma unroll 1
                     for (int i = lane; i < parts; i += 32) {
-                        const float2 ml = __ldcg(&p.part_ml[slot_of(i) * 16 + row]);
+                        const float2 ml = i == lane ? x : __ldcg(&p.part_ml[slot_of(i) * 16 + row]);
                         const float w = exp2f(ml.x - M);
                         weight[row * parts + i] = w;
                         L = fmaf(ml.y, w, L);
