@@ -49,12 +49,16 @@ template <int D> struct PromptSmem {
     static constexpr int kSubs = D == 256 ? 2 : 1;
     static constexpr int kQ = 128 * D;                         // one part of one query tile
     static constexpr int kK = kTok * D, kKStages = D == 256 ? 2 : 3;
-    static constexpr int kRaw = kHalf * D, kRawStages = D == 256 ? 2 : 4;
+    static constexpr int kRaw = kHalf * D, kRawStages = D == 256 ? 2 : 3;
     static constexpr int kV = kHalf * D * 2, kVStages = D == 256 ? 2 : 4;
     static constexpr int off_k = kTiles * 2 * kQ;
     static constexpr int off_raw = off_k + kKStages * kK;
     static constexpr int off_v = off_raw + kRawStages * kRaw;
-    static constexpr int off_misc = off_v + kVStages * kV;
+    // 32 output columns of every row, padded, for each softmax warp: of their own, or, at head dimension 256, in the
+    // queries' place once no product reads them
+    static constexpr int kPitch = 80, kStaging = D == 256 ? 0 : 8 * 32 * kPitch;
+    static constexpr int off_staging = D == 256 ? 0 : off_v + kVStages * kV;
+    static constexpr int off_misc = off_v + kVStages * kV + kStaging;
     struct Misc {
         uint64_t q_full, o_free;
         uint64_t k_full[kKStages], k_empty[kKStages];
@@ -115,6 +119,11 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+    return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 r;
@@ -343,17 +352,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         int w = 0;       // items of the CTA so far
         int checked = -1;
         bool bad_pages = false;
-        for (int unit = 0; alive && line.next(seg); ++unit) {
+        // Rows of the query tile that this warp splits into hi + lo, D / 8 lanes a row, 16 bytes each.  The bytes come
+        // asynchronously, four elements to where their hi will lie and four to where their lo will, for all rows at
+        // once, and, where the tile's place is free by then, while the unit before ends.
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = kSplit ? 16 : 32;
+        const int sub = lane / kLanes, c8 = lane % kLanes, row0 = kSplit ? warp * 16 : (warp & 3) * 32;
+        const uint32_t hi_at = base + q_tile * 2 * S::kQ, lo_at = hi_at + S::kQ;
+        // token and head of row x of a tile, from its first row's
+        auto place = [&](const Segment &sg, int token0, int head0, int x, int &token, int &h) {
+            const int y = head0 + x, up = p.group == 1 ? y : int(__umulhi(uint32_t(y), p.group_inverse));
+            token = token0 + up, h = sg.head * p.group + (y - up * p.group);
+        };
+        auto fetch_queries = [&](const Segment &sg) {
+            const int g0 = sg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
+#pragma unroll 1
+            for (int i = sub; i < kMine; i += kAtOnce) {
+                const int x = q_tile * 128 + row0 + i;
+                int tx, hx;
+                place(sg, token0, head0, x, tx, hx);
+                const bool there = x < sg.rows;
+                const __nv_bfloat16 *src = p.q + (there ? (long long)(sg.bos + tx) * p.q_stride + hx * D + 8 * c8 : 0);
+                const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
+                const int bytes = there ? 8 : 0;  // zeros where there is no row
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(hi_at + at), "l"(src), "r"(bytes) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(lo_at + at), "l"(src + 4), "r"(bytes) : "memory");
+            }
+        };
+        bool more = line.next(seg);
+        if (more) fetch_queries(seg);
+        for (int unit = 0; alive && more; ++unit) {
             const int tiles = seg.b1 - seg.b0;
-            // the tile's first row's token and head of the group, and from there those of row x
             const int g0 = seg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
-            auto place = [&](int x, int &token, int &h) {
-                const int y = head0 + x, up = p.group == 1 ? y : int(__umulhi(uint32_t(y), p.group_inverse));
-                token = token0 + up, h = seg.head * p.group + (y - up * p.group);
-            };
             const int r = q_tile * 128 + row;
             int token, head;
-            place(r, token, head);
+            place(seg, token0, head0, r, token, head);
             const bool real = r < seg.rows;
             const int seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
             if (checked != seg.seq) {
@@ -368,54 +400,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bad_pages && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
                 checked = seg.seq;
             }
-            // the queries as hi + lo: D / 8 lanes read a row, 16 bytes each
+            // the queries as hi + lo
             float row_scale;
             {
-                constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4, kMine = kSplit ? 16 : 32;
-                const int sub = lane / kLanes, c8 = lane % kLanes, row0 = kSplit ? warp * 16 : (warp & 3) * 32;
-                const uint32_t hi_at = base + q_tile * 2 * S::kQ, lo_at = hi_at + S::kQ;
                 float *scales = misc.row_scale[q_tile];
                 const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
-#pragma unroll 1
-                for (int i0 = 0; i0 < kMine; i0 += kAtOnce * kBatch) {
-                    uint4 in[kBatch];
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+#pragma unroll 4
+                for (int i = sub; i < kMine; i += kAtOnce) {
+                    const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
+                    const uint2 a = lds64(hi_at + at), b = lds64(lo_at + at);
+                    const uint32_t x[4] = {a.x, a.y, b.x, b.y};
+                    float f[8], top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int x = q_tile * 128 + row0 + i0 + i * kAtOnce + sub;
-                        int tx, hx;
-                        place(x, tx, hx);
-                        in[i] = make_uint4(0, 0, 0, 0);
-                        if (x < seg.rows)
-                            in[i] = *reinterpret_cast<const uint4 *>(p.q + (long long)(seg.bos + tx) * p.q_stride + hx * D + 8 * c8);
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+                        top = fmaxf(top, fabsf(f[e]));
                     }
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r_at = row0 + i0 + i * kAtOnce + sub;
-                        const uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                        float f[8], top = 0.f;
+                    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float down = row_down(top), factor = down * sign;
+                    uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
-                            top = fmaxf(top, fabsf(f[e]));
-                        }
+                    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                        for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float down = row_down(top), factor = down * sign;
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
-                            hi[e] = to_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                            const float2 a = e4m3x2_to_float2(hi[e]), b = e4m3x2_to_float2(hi[e] >> 16);
-                            lo[e] = to_e4m3x4(f[4 * e] - a.x, f[4 * e + 1] - a.y, f[4 * e + 2] - b.x, f[4 * e + 3] - b.y);
-                        }
-                        const uint32_t at = chunk8_at<D>(128, r_at, c8 >> 1) + (c8 & 1) * 8;
-                        sts64(hi_at + at, hi[0], hi[1]);
-                        sts64(lo_at + at, lo[0], lo[1]);
-                        // the inverse of a power of two, by its exponent; every lane of the row writes the same
-                        scales[r_at] = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
+                        for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
+                        hi[e] = to_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
+                        lo[e] = to_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
                     }
+                    sts64(hi_at + at, hi[0], hi[1]);
+                    sts64(lo_at + at, lo[0], lo[1]);
+                    // the inverse of a power of two, by its exponent; every lane of the row writes the same
+                    scales[row0 + i] = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
                 }
                 tc::fence_async_smem();
                 tc::mbar_arrive(&misc.q_full);
@@ -537,6 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int last = w + (tiles - 1) * NQ + q_tile;
             w += tiles * NQ;
             if (!alive) break;
+            // the next unit's queries: every product with this one's is done
+            Segment next;
+            if (!kSplit) {
+                more = line.next(next);
+                if (more) fetch_queries(next);
+            }
             if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
                 float(*sums)[128] = misc.top[(last + 1) & 1];
                 sums[group][row] = l;
@@ -551,6 +574,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long out_row = (long long)(seg.bos + token) * p.h_q + head;
             const int slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
+            // outputs: a warp's 32 rows by 32 columns through shared memory, so that four lanes write a row's 64 bytes
+            uint8_t *staging = smem + S::off_staging + warp * 32 * S::kPitch;
+            long long to[4];  // where rows lane / 4 + 8 i go, or -1
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to[i] = __shfl_sync(0xffffffffu, real && !bad_pages ? out_row : -1ll, (lane >> 2) + 8 * i);
+                if (to[i] >= 0) to[i] = to[i] * D + out0 + (lane & 3) * 8;
+            }
             // part sums: [slot][tile][D / 4][128 rows] of four columns, so that neighbouring rows lie together
             float4 *part = reinterpret_cast<float4 *>(p.parts) + ((long long)(slot * NQ + q_tile) * D + out0) / 4 * 128 + row;
             const bool poisoned = misc.poison[unit % kPoisonSlots] == unit + 1;
@@ -571,22 +602,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) y[e] = hit >> e & 1 ? 0x7fc00000u : y[e];
                 }
                 if (seg.whole) {
-                    // half of the thread's columns at a time, padded rows in the query tile's place, which no product
-                    // reads any more
-                    if (c % (kOut / 2) == 0) tc::bulk_wait_read();
-                    uint8_t *mine = smem + group * (kSplit ? 1 : 2) * S::kQ + row * (kOut + 16);
+                    const uint32_t mine = tc::smem_u32(staging) + lane * S::kPitch;
+                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        sts128(tc::smem_u32(mine) + (c % (kOut / 2) + e) * 2,
-                               pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                        sts128(mine + e * 2, pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
                                pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
                                pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
                                pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
-                    if ((c + 32) % (kOut / 2) == 0) {
-                        tc::fence_async_smem();
-                        if (real && !bad_pages)
-                            tc::bulk_store(p.o + out_row * D + out0 + (c >= kOut / 2 ? kOut / 2 : 0), mine, kOut);
-                        tc::bulk_commit();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (lane & 3) * 16);
+                        if (to[i] >= 0) *reinterpret_cast<uint4 *>(p.o + to[i] + c) = v;
                     }
                 } else {
 #pragma unroll
@@ -599,55 +627,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_arrive(&misc.o_free);
             if (seg.whole) {
                 if (real && !bad_pages && p.lse && out0 == 0) p.lse[out_row] = log_sum(m, l);
-                tc::bulk_wait_read();
-                named_sync(bar_id, bar_count);  // the rows' place is the queries' again
-                continue;
-            }
-            if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
-            named_sync(bar_id, bar_count);
-            if (row == 0 && out0 == 0) {
-                int *ticket = &p.tickets[first_cta * NQ + q_tile];
-                const bool mine = take_ticket(ticket) == last_cta - first_cta;
-                if (mine) *ticket = 0;
-                misc.ticket[q_tile] = mine;
-            }
-            named_sync(bar_id, bar_count);
-            if (misc.ticket[q_tile] && real && !bad_pages) {
-                const int parts = last_cta - first_cta + 1;
-                auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
-                float M = kNone, L = 0.f;
-#pragma unroll 1
-                for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
-#pragma unroll 1
-                for (int i = 0; i < parts; ++i) {
-                    const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
-                    L = fmaf(ml.y, exp2f(ml.x - M), L);
+            } else {
+                if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
+                named_sync(bar_id, bar_count);
+                if (row == 0 && out0 == 0) {
+                    int *ticket = &p.tickets[first_cta * NQ + q_tile];
+                    const bool mine = take_ticket(ticket) == last_cta - first_cta;
+                    if (mine) *ticket = 0;
+                    misc.ticket[q_tile] = mine;
                 }
-                const float one = L == 0.f ? 0.f : 1.f / L;
+                named_sync(bar_id, bar_count);
+                if (misc.ticket[q_tile] && real && !bad_pages) {
+                    const int parts = last_cta - first_cta + 1;
+                    auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
+                    float M = kNone, L = 0.f;
 #pragma unroll 1
-                for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
-                    float4 sum[8] = {};
+                    for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
 #pragma unroll 1
                     for (int i = 0; i < parts; ++i) {
-                        const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
-                        const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 v = __ldcg(src + e * 128);
-                            sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
-                            sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
-                        }
+                        const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
+                        L = fmaf(ml.y, exp2f(ml.x - M), L);
                     }
+                    const float one = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+                    for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
+                        float4 sum[8] = {};
+#pragma unroll 1
+                        for (int i = 0; i < parts; ++i) {
+                            const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
+                            const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        *reinterpret_cast<uint4 *>(p.o + out_row * D + 4 * (c + e)) =
-                            make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
-                                       pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
-                                       pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = __ldcg(src + e * 128);
+                                sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
+                                sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2)
+                            *reinterpret_cast<uint4 *>(p.o + out_row * D + 4 * (c + e)) =
+                                make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
+                                           pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
+                                           pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
+                    }
+                    if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
                 }
-                if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
+                named_sync(bar_id, bar_count);  // the ticket may be written again
             }
-            named_sync(bar_id, bar_count);  // the ticket may be written again
+            if (kSplit) {
+                named_sync(bar_id, bar_count);  // the staging is the queries' again
+                more = line.next(next);
+                if (more) fetch_queries(next);
+            }
+            seg = next;
         }
     }
 done:
