@@ -35,6 +35,11 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
     return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
 }
+// The same without the care for infinities, which are clipped too.
+__device__ __forceinline__ uint32_t clipped_e4m3x4(float a, float b, float c, float d) {
+    return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) |
+           (uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16);
+}
 // Two e4m3 bytes (the lower 16 bits) to half precision, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     uint32_t r;

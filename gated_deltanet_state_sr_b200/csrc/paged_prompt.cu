@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto fetch_queries = [&](const Segment &sg) {
             const int g0 = sg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = sub; i < kMine; i += kAtOnce) {
                 const int x = q_tile * 128 + row0 + i;
                 int tx, hx;
@@ -425,14 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 2; ++e) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
-                        hi[e] = to_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        hi[e] = clipped_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
                         const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
-                        lo[e] = to_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
+                        lo[e] = clipped_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
                     }
                     sts64(hi_at + at, hi[0], hi[1]);
                     sts64(lo_at + at, lo[0], lo[1]);
-                    // the inverse of a power of two, by its exponent; every lane of the row writes the same
-                    scales[row0 + i] = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
+                    // the inverse of a power of two, by its exponent; every lane of the row writes the same.  An infinity,
+                    // which the conversion clips, spoils its row here (a NaN does so as a NaN).
+                    const float one = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
+                    scales[row0 + i] = top <= 3.402823466e38f ? one : __uint_as_float(0x7fc00000u);
                 }
                 tc::fence_async_smem();
                 tc::mbar_arrive(&misc.q_full);

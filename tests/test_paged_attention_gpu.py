@@ -205,13 +205,15 @@ def test_nan_bytes_reach_the_rows_that_see_them_and_no_others(sr):
 
 
 def test_queries_that_are_not_finite_spoil_their_own_rows(sr):
-    c = make([3, 1], [100, 90], 4, 2, 128, 64, seed=14)
-    clean, _ = call(sr, c)
-    c["q"][1, 2, 7], c["q"][3, 0, 0] = float("nan"), float("inf")
-    o, _ = call(sr, c)
-    spoilt = torch.zeros(4, 4, dtype=torch.bool)
-    spoilt[1, 2] = spoilt[3, 0] = True
-    assert bool(torch.isnan(o[spoilt.cuda()]).all()) and torch.equal(o[~spoilt.cuda()], clean[~spoilt.cuda()])
+    for new in ([3, 1], [40, 1]):
+        c = make(new, [100, 90], 4, 2, 128, 64, seed=14)
+        clean, _ = call(sr, c)
+        c["q"][1, 2, 7], c["q"][new[0], 0, 0], c["q"][2, 1, 100] = float("nan"), float("inf"), float("-inf")
+        o, lse = call(sr, c)
+        spoilt = torch.zeros(sum(new), 4, dtype=torch.bool, device="cuda")
+        spoilt[1, 2] = spoilt[new[0], 0] = spoilt[2, 1] = True
+        assert bool(torch.isnan(o[spoilt]).all()) and bool(torch.isnan(lse[spoilt]).all())
+        assert torch.equal(o[~spoilt], clean[~spoilt])
 
 
 def test_strided_queries_no_lse_and_given_outputs(sr):
