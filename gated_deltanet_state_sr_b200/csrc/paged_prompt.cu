@@ -17,9 +17,9 @@
 // A CTA walks its part of the line of blocks (paged_attention.cuh).  Its warps:
 //   two groups of four: softmax, a row per thread, for two tiles of query rows
 //     (head dimension 256: one tile, whose scores have two buffers; the groups
-//     take half of a tile's columns each and exchange the rows' largest);
-//   one group of four: a unit's queries into their two parts, values to half
-//     precision;
+//     take half of a tile's columns each and exchange the rows' largest), and the
+//     queries' split at the start of a unit;
+//   one group of four: values to half precision;
 //   a warp that issues the products, S of two items ahead of P V of one;
 //   a warp that loads pages of keys, and one for values.
 // Tensor memory: two buffers of scores (128 columns each) and the sums O (two
@@ -45,9 +45,6 @@ constexpr int kPoisonSlots = 16;
 template <int D> struct PromptSmem {
     static constexpr int kTiles = D == 256 ? 1 : 2;            // query tiles
     static constexpr int kRows = 128 * kTiles;
-    // Units whose rows' factors are held: a unit's queries are split while the softmax groups may still end the one
-    // before, but for head dimension 256, whose query tile they have to leave first.
-    static constexpr int kScales = D == 256 ? 1 : 2;
     static constexpr int kSub = D == 64 ? 64 : 128;            // bytes of an 8-bit row in shared memory
     static constexpr int kSubs = D == 256 ? 2 : 1;
     static constexpr int kQ = 128 * D;                         // one part of one query tile
@@ -63,7 +60,7 @@ template <int D> struct PromptSmem {
     static constexpr int off_staging = D == 256 ? 0 : off_v + kVStages * kV;
     static constexpr int off_misc = off_v + kVStages * kV + kStaging;
     struct Misc {
-        uint64_t q_full, q_empty, o_free;
+        uint64_t q_full, o_free;
         uint64_t k_full[kKStages], k_empty[kKStages];
         uint64_t raw_full[kRawStages], raw_empty[kRawStages];
         uint64_t v_full[kVStages], v_empty[kVStages];
@@ -74,7 +71,7 @@ template <int D> struct PromptSmem {
         };
         uint32_t tmem;
         int poison[kPoisonSlots];
-        float row_scale[kScales][kTiles][128];
+        float row_scale[kTiles][128];
         int ticket[2];
     };
     static constexpr int bytes = off_misc + int(sizeof(Misc));
@@ -139,68 +136,6 @@ __device__ __forceinline__ int page_at(const AttnParams &p, int seq, int token) 
     return page < 0 || page >= p.n_pages ? 0 : page;  // the output of such a sequence is not written
 }
 
-// Token and head of row x of a tile, from its first row's.
-__device__ __forceinline__ void place_of(const AttnParams &p, const Segment &seg, int token0, int head0, int x, int &token,
-                                         int &head) {
-    const int y = head0 + x, up = p.group == 1 ? y : int(__umulhi(uint32_t(y), p.group_inverse));
-    token = token0 + up, head = seg.head * p.group + (y - up * p.group);
-}
-
-// A unit's query rows into shared memory as hi + lo, by one warpgroup: D / 8 lanes a row, 16 bytes each.  The bytes
-// come asynchronously, four elements to where their hi will lie and four to where their lo will, all rows at once.
-template <int D, int TILES>
-__device__ __forceinline__ void split_queries(const AttnParams &p, const Segment &seg, uint32_t base, float (*scales)[128]) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = 32 * TILES, kQ = 128 * D;
-    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, sub = lane / kLanes, c8 = lane % kLanes;
-    const int g0 = seg.tile * 128 * TILES, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
-    auto hi_of = [&](int x) { return base + (x >> 7) * 2 * kQ + chunk8_at<D>(128, x & 127, c8 >> 1) + (c8 & 1) * 8; };
-#pragma unroll 4
-    for (int i = sub; i < kMine; i += kAtOnce) {
-        const int x = warp * kMine + i;
-        int token, head;
-        place_of(p, seg, token0, head0, x, token, head);
-        const bool there = x < seg.rows;
-        const __nv_bfloat16 *src = p.q + (there ? (long long)(seg.bos + token) * p.q_stride + head * D + 8 * c8 : 0);
-        const uint32_t at = hi_of(x);
-        const int bytes = there ? 8 : 0;  // zeros where there is no row
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(at), "l"(src), "r"(bytes) : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(at + kQ), "l"(src + 4), "r"(bytes) : "memory");
-    }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
-    const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
-#pragma unroll 4
-    for (int i = sub; i < kMine; i += kAtOnce) {
-        const int row = warp * kMine + i;
-        const uint32_t at = hi_of(row);
-        const uint2 a = lds64(at), b = lds64(at + kQ);
-        const uint32_t x[4] = {a.x, a.y, b.x, b.y};
-        float f[8], top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
-            top = fmaxf(top, fabsf(f[e]));
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float down = row_down(top), factor = down * sign;
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
-            hi[e] = clipped_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-            const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
-            lo[e] = clipped_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
-        }
-        sts64(at, hi[0], hi[1]);
-        sts64(at + kQ, lo[0], lo[1]);
-        // the inverse of a power of two, by its exponent; every lane of the row writes the same.  An infinity, which the
-        // conversion clips, spoils its row here (a NaN does so as a NaN).
-        const float one = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
-        scales[row >> 7][row & 127] = top <= 3.402823466e38f ? one : __uint_as_float(0x7fc00000u);
-    }
-}
-
 // Which of the columns c .. c + 31 hold a NaN among tokens t0 .. t1 - 1.
 __device__ __forceinline__ uint32_t nan_columns(const AttnParams &p, const Segment &seg, int t0, int t1, int c, int d) {
     uint32_t hit = 0;
@@ -226,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = tc::smem_u32(smem);
 
     if (threadIdx.x == 0) {
-        tc::mbar_init(&misc.q_full, 128);
-        tc::mbar_init(&misc.q_empty, kSplit ? 257 : 1);  // its last product, and the outputs' way through its place
+        tc::mbar_init(&misc.q_full, 256);
         tc::mbar_init(&misc.o_free, 256);
         for (int i = 0; i < S::kKStages; ++i) tc::mbar_init(&misc.k_full[i], 1), tc::mbar_init(&misc.k_empty[i], 1);
         for (int i = 0; i < S::kRawStages; ++i) tc::mbar_init(&misc.raw_full[i], 1), tc::mbar_init(&misc.raw_empty[i], 128);
@@ -307,8 +241,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::mma_commit(&misc.pv_done[b]);
                     }
                     if (i < items && !scores(i)) break;
-                    if (i == items - 1 || items == 0) tc::mma_commit(&misc.q_empty);
-                    if (items == 0) break;
                 }
                 // a unit without tiles keeps the count of the sums' releases
                 if (items == 0 && unit && !wait(misc.o_free, unit - 1)) break;
@@ -344,16 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
         }
     } else if (warp >= 8) {
-        // ---- a unit's queries as hi + lo, once its place is free, while the softmax groups end the unit before; then
-        // values to half precision: token rows of 64 columns, 128-byte swizzle, the layout of an MN-major operand
+        // ---- values to half precision: token rows of 64 columns, 128-byte swizzle, the layout of an MN-major operand
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kConvertRegs));
         const int t = threadIdx.x - 256;
         int vt = 0;
         for (int unit = 0; alive && line.next(seg); ++unit) {
-            if (unit && !wait(misc.q_empty, unit - 1)) break;
-            split_queries<D, NQ>(p, seg, base, misc.row_scale[unit % S::kScales]);
-            tc::fence_async_smem();
-            tc::mbar_arrive(&misc.q_full);
             const int most = line_seen(p, seg, seg.rows - 1, S::kRows), least = line_seen(p, seg, 0, S::kRows);
 #pragma unroll 1
             for (int tok0 = seg.b0 * kTok; tok0 < seg.b1 * kTok; tok0 += kHalf, ++vt) {
@@ -425,12 +352,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         int w = 0;       // items of the CTA so far
         int checked = -1;
         bool bad_pages = false;
-        for (int unit = 0; alive && line.next(seg); ++unit) {
+        // Rows of the query tile that this warp splits into hi + lo, D / 8 lanes a row, 16 bytes each.  The bytes come
+        // asynchronously, four elements to where their hi will lie and four to where their lo will, for all rows at
+        // once, and, where the tile's place is free by then, while the unit before ends.
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = kSplit ? 16 : 32;
+        const int sub = lane / kLanes, c8 = lane % kLanes, row0 = kSplit ? warp * 16 : (warp & 3) * 32;
+        const uint32_t hi_at = base + q_tile * 2 * S::kQ, lo_at = hi_at + S::kQ;
+        // token and head of row x of a tile, from its first row's
+        auto place = [&](const Segment &sg, int token0, int head0, int x, int &token, int &h) {
+            const int y = head0 + x, up = p.group == 1 ? y : int(__umulhi(uint32_t(y), p.group_inverse));
+            token = token0 + up, h = sg.head * p.group + (y - up * p.group);
+        };
+        auto fetch_queries = [&](const Segment &sg) {
+            const int g0 = sg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
+#pragma unroll 4
+            for (int i = sub; i < kMine; i += kAtOnce) {
+                const int x = q_tile * 128 + row0 + i;
+                int tx, hx;
+                place(sg, token0, head0, x, tx, hx);
+                const bool there = x < sg.rows;
+                const __nv_bfloat16 *src = p.q + (there ? (long long)(sg.bos + tx) * p.q_stride + hx * D + 8 * c8 : 0);
+                const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
+                const int bytes = there ? 8 : 0;  // zeros where there is no row
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(hi_at + at), "l"(src), "r"(bytes) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(lo_at + at), "l"(src + 4), "r"(bytes) : "memory");
+            }
+        };
+        bool more = line.next(seg);
+        if (more) fetch_queries(seg);
+        for (int unit = 0; alive && more; ++unit) {
             const int tiles = seg.b1 - seg.b0;
             const int g0 = seg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
             const int r = q_tile * 128 + row;
             int token, head;
-            place_of(p, seg, token0, head0, r, token, head);
+            place(seg, token0, head0, r, token, head);
             const bool real = r < seg.rows;
             const int seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
             if (checked != seg.seq) {
@@ -445,8 +400,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bad_pages && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
                 checked = seg.seq;
             }
-            if (!wait(misc.q_full, unit)) break;
-            const float row_scale = misc.row_scale[unit % S::kScales][q_tile][row];
+            // the queries as hi + lo
+            float row_scale;
+            {
+                float *scales = misc.row_scale[q_tile];
+                const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+#pragma unroll 4
+                for (int i = sub; i < kMine; i += kAtOnce) {
+                    const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
+                    const uint2 a = lds64(hi_at + at), b = lds64(lo_at + at);
+                    const uint32_t x[4] = {a.x, a.y, b.x, b.y};
+                    float f[8], top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+                        top = fmaxf(top, fabsf(f[e]));
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float down = row_down(top), factor = down * sign;
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
+                        hi[e] = clipped_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
+                        lo[e] = clipped_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
+                    }
+                    sts64(hi_at + at, hi[0], hi[1]);
+                    sts64(lo_at + at, lo[0], lo[1]);
+                    // the inverse of a power of two, by its exponent; every lane of the row writes the same.  An infinity,
+                    // which the conversion clips, spoils its row here (a NaN does so as a NaN).
+                    const float one = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
+                    scales[row0 + i] = top <= 3.402823466e38f ? one : __uint_as_float(0x7fc00000u);
+                }
+                tc::fence_async_smem();
+                tc::mbar_arrive(&misc.q_full);
+                if (kSplit) named_sync(bar_id, bar_count); else __syncwarp();
+                row_scale = scales[row];
+            }
+
             float m = kNone, l = 0.f;
             // Lane g of every eight (four) holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
             // columns, loaded a tile ahead, their page two.
@@ -561,6 +556,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int last = w + (tiles - 1) * NQ + q_tile;
             w += tiles * NQ;
             if (!alive) break;
+            // the next unit's queries: every product with this one's is done
+            Segment next;
+            if (!kSplit) {
+                more = line.next(next);
+                if (more) fetch_queries(next);
+            }
             if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
                 float(*sums)[128] = misc.top[(last + 1) & 1];
                 sums[group][row] = l;
@@ -675,7 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 named_sync(bar_id, bar_count);  // the ticket may be written again
             }
-            if (kSplit) tc::mbar_arrive(&misc.q_empty);  // the staging is the queries' again
+            if (kSplit) {
+                named_sync(bar_id, bar_count);  // the staging is the queries' again
+                more = line.next(next);
+                if (more) fetch_queries(next);
+            }
+            seg = next;
         }
     }
 done:
