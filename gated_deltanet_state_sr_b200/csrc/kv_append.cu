@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
             for (int i = 0; i < kBatch; ++i) {
                 const int t = min(t0 + sub + i * kAtOnce, n - 1);
                 const __nv_bfloat16 *row = src + t * stride;
+                in[i][0] = in[i][1] = make_uint2(0, 0);
+                if (!SR_IN_BOUNDS(tok0 + t, p.total, p.status)) continue;
                 in[i][0] = *reinterpret_cast<const uint2 *>(row + w.lo);
                 in[i][1] = *reinterpret_cast<const uint2 *>(row + w.hi);
             }
@@ -163,12 +165,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
             __nv_bfloat16 *dst = p.q_out + (long long)tok0 * p.q_out_stride + h * D;
             walk(p.q + (long long)tok0 * p.q_stride + h * D, p.q_stride, u, std::true_type{}, [&](int t, const float(&f)[8]) {
                 __nv_bfloat16 *out = dst + t * p.q_out_stride;
+                if (!SR_IN_BOUNDS(tok0 + t, p.total, p.status)) return;
                 *reinterpret_cast<uint2 *>(out + u.lo) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
                 *reinterpret_cast<uint2 *>(out + u.hi) = make_uint2(pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
             });
             continue;
         }
-        if (!page_ok) continue;
+        if (!page_ok || !SR_IN_BOUNDS(slot, p.max_pages, p.status)) continue;
         const bool key = item < p.h_kv;
         const int h = key ? item : item - p.h_kv;
         const Unit w = key ? u : plain;
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(AppendParams p) {
         const float inv = 1.f / kept;
         auto store = [&](int t, const float(&f)[8]) {
             uint8_t *out = cache + (old + t) * D;
+            if (!SR_IN_BOUNDS(old + t, p.page, p.status)) return;
             *reinterpret_cast<uint32_t *>(out + w.lo) = paged::to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
             *reinterpret_cast<uint32_t *>(out + w.hi) = paged::to_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
         };

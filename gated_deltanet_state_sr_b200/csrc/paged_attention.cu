@@ -32,6 +32,7 @@ sr_status validate(const sr_paged_attention_args *a) {
     if (a->h_q / a->h_kv > 64) return set_error(SR_ERR_UNSUPPORTED, "h_q / h_kv > 64");
     if ((long long)a->total_tokens * (a->h_q / a->h_kv) > (1 << 30))
         return set_error(SR_ERR_UNSUPPORTED, "total_tokens * h_q / h_kv > 2^30");
+    if (a->n_pages == 0) return set_error(SR_ERR_INVALID_ARG, "the cache has no pages");
     if ((long long)a->n_pages * a->h_kv * a->page_size > INT32_MAX)
         return set_error(SR_ERR_UNSUPPORTED, "n_pages * h_kv * page_size > 2^31 - 1");
     if (a->q_stride < int64_t(a->h_q) * a->head_dim || a->q_stride % 8 || !aligned(a->q, 16))
@@ -80,7 +81,6 @@ extern "C" sr_status sr_paged_attention(const sr_paged_attention_args *a, void *
     // boxes of a page's rows (64 at most) and 128 columns (64 at head dimension 64)
     const int rows = a->n_pages * a->h_kv * a->page_size, box = a->page_size < 64 ? a->page_size : 64;
     CUtensorMap km, vm;
-    if (rows == 0) return set_error(SR_ERR_INVALID_ARG, "the cache has no pages");
     if (!make_map_cache(&km, a->k_cache, rows, a->head_dim, box) || !make_map_cache(&vm, a->v_cache, rows, a->head_dim, box))
         return set_error(SR_ERR_CUDA, "sr_paged_attention: encoding the tensor maps");
     e = paged::few_rows(a) ? paged::attend_rows(km, vm, p, a->head_dim, st)

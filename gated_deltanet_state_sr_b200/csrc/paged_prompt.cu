@@ -40,7 +40,7 @@ constexpr int kUnitStart = 512; // what a unit costs beside its tiles, in tokens
 // 256 x 160 + 128 x 96 + 128 x 96 = 512 x 128, what the block is launched with.
 constexpr int kSoftmaxRegs = 160, kConvertRegs = 96, kIssueRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= 512 * 128, "the split draws on the launch's");
-constexpr int kPoisonSlots = 16;
+constexpr int kPoisonSlots = 8;  // units with tiles that the values may be ahead of the sums: fewer, by their ring
 
 template <int D> struct PromptSmem {
     static constexpr int kTiles = D == 256 ? 1 : 2;            // query tiles
@@ -279,8 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- values to half precision: token rows of 64 columns, 128-byte swizzle, the layout of an MN-major operand
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kConvertRegs));
         const int t = threadIdx.x - 256;
-        int vt = 0;
-        for (int unit = 0; alive && line.next(seg); ++unit) {
+        int vt = 0, filled = 0;  // filled: units with tiles so far
+        while (alive && line.next(seg)) {
+            const int unit = filled;
+            filled += seg.b1 > seg.b0;
             const int most = line_seen(p, seg, seg.rows - 1, S::kRows), least = line_seen(p, seg, 0, S::kRows);
 #pragma unroll 1
             for (int tok0 = seg.b0 * kTok; tok0 < seg.b1 * kTok; tok0 += kHalf, ++vt) {
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int bar_id = kSplit ? 1 : 1 + group, bar_count = kSplit ? 256 : 128;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t o_at = tmem + lanes + 256 + q_tile * 128 + out0;
-        int w = 0;       // items of the CTA so far
+        int w = 0, filled = 0;  // items of the CTA, units with tiles so far
         int checked = -1;
         bool bad_pages = false;
         // Rows of the query tile that this warp splits into hi + lo, D / 8 lanes a row, 16 bytes each.  The bytes come
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = q_tile * 128 + row;
             int token, head;
             place(seg, token0, head0, r, token, head);
-            const bool real = r < seg.rows;
+            const bool real = r < seg.rows && SR_IN_BOUNDS(seg.bos + token, p.total, p.status);
             const int seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
             if (checked != seg.seq) {
                 bool bad = false;
@@ -586,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // part sums: [slot][tile][D / 4][128 rows] of four columns, so that neighbouring rows lie together
             float4 *part = reinterpret_cast<float4 *>(p.parts) + ((long long)(slot * NQ + q_tile) * D + out0) / 4 * 128 + row;
-            const bool poisoned = misc.poison[unit % kPoisonSlots] == unit + 1;
+            const bool poisoned = tiles > 0 && misc.poison[filled % kPoisonSlots] == filled + 1;
+            filled += tiles > 0;
             const int edge0 = line_seen(p, seg, 0, S::kRows) / kHalf * kHalf;  // the first stage that rows see differently
 #pragma unroll 1
             for (int c = 0; c < kOut; c += 32) {

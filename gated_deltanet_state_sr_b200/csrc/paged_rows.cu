@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = 8 * n + 2 * j + e;
-                    if (row >= seg.rows) continue;
+                    if (row >= seg.rows || !SR_IN_BOUNDS(out_row(row), (long long)p.total * p.h_q, p.status)) continue;
                     const float inv = l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
                     const long long to = out_row(row);
 #pragma unroll
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(RowsShape<D, NT>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = 8 * n + 2 * j + e;
-                        if (row >= seg.rows) continue;
+                        if (row >= seg.rows || !SR_IN_BOUNDS(part_slot, 2 * kRowsMaxCtas, p.status)) continue;
                         float *out = p.parts + ((long long)part_slot * 16 + row) * D;
 #pragma unroll
                         for (int t = 0; t < D / 8; t += 4)

@@ -593,7 +593,7 @@ SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, si
  *   kv_lens, block_table, k_cache, v_cache, k_scale, v_scale  as in
  *              sr_kv_append; a scale outside 2^-32..2^32 is taken as the nearer
  *              bound
- *   o          [total_tokens, h_q, head_dim] bf16
+ *   o          [total_tokens, h_q, head_dim] bf16; must not overlap q
  *   lse        [total_tokens, h_q] fp32, may be NULL: log sum_t exp(scale q . k_t)
  *   scale      0 selects 1/sqrt(head_dim)
  * Scores, softmax statistics and sums are fp32; the weights meet the tensor
@@ -603,7 +603,7 @@ SR_API sr_status sr_kv_append(const sr_kv_append_args *args, void *workspace, si
  * Tokens that a row does not see have no part in it, whatever they hold (NaN
  * bytes included).  The same call gives the same bits.
  * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64 or 128; h_q / h_kv
- * up to 64; n_pages * h_kv * page_size < 2^31.  max_seqlen bounds a sequence's
+ * up to 64; n_pages > 0, n_pages * h_kv * page_size < 2^31.  max_seqlen bounds a sequence's
  * new tokens, max_kvlen its cached ones.  A page number outside [0, n_pages)
  * among a sequence's ceil(kv_lens[n] / page_size) skips the sequence and sets
  * SR_DEV_BAD_INDEX; a kv_lens entry below 0, above max_kvlen or above max_pages *

@@ -382,6 +382,7 @@ def _paged_attention(**kw):
     ("max_kvlen", -1, sr.SR_ERR_INVALID_ARG),
     ("max_pages", 1 << 28, sr.SR_ERR_UNSUPPORTED),
     ("n_pages", 1 << 25, sr.SR_ERR_UNSUPPORTED),  # 2^32 rows of the cache
+    ("n_pages", 0, sr.SR_ERR_INVALID_ARG),
     ("total_tokens", 1 << 30, sr.SR_ERR_UNSUPPORTED),
     ("max_seqlen", 101, sr.SR_ERR_INVALID_ARG),
     ("scale", float("inf"), sr.SR_ERR_INVALID_ARG),

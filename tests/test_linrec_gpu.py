@@ -90,7 +90,7 @@ LENGTHS = [
 
 
 @pytest.mark.parametrize("lens", LENGTHS, ids=str)
-@pytest.mark.parametrize("D", [1, 37, 64, 130])
+@pytest.mark.parametrize("D", [1, 8, 37, 64, 130, 200])
 @pytest.mark.parametrize("types", [(BF, BF), (BF, F32), (F32, F32)], ids=["bf16", "bf16_g32", "fp32"])
 def test_forward_and_backward(sr, lens, D, types):
     c = make(lens, D, *types, h0=D != 37, seed=D)

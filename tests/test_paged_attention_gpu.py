@@ -204,6 +204,16 @@ def test_nan_bytes_reach_the_rows_that_see_them_and_no_others(sr):
         assert bool(torch.isnan(o[new - 1, 0]).all()) and bool(torch.isnan(lse[new - 1, 0]))
 
 
+def test_nan_bytes_beside_many_rows_that_see_nothing(sr):
+    """More query tiles without a cached token, between those that have some, than any ring of the kernel holds."""
+    new = [200] + [130] * 40 + [200]
+    c = make(new, [200] + [0] * 40 + [200], 4, 2, 128, 64, seed=22)
+    for n in (0, 41):
+        c["v_cache"][c["table"][n, 3], 1, 5, 9] = 0x7f  # token 197
+    o, _ = check(sr, c)
+    assert bool(torch.isnan(o[197:200, 2:, 9]).all()) and bool(torch.isnan(o[-3:, 2:, 9]).all()) and int(torch.isnan(o).sum()) == 12
+
+
 def test_queries_that_are_not_finite_spoil_their_own_rows(sr):
     for new in ([3, 1], [40, 1]):
         c = make(new, [100, 90], 4, 2, 128, 64, seed=14)
