@@ -330,7 +330,7 @@ _lrb = _sig("sr_linrec_backward", _i32, ctypes.POINTER(LinrecGradArgs), _vp, cty
 
 def _want(t, name, dtypes, shape, device):
     """Checks an optional or required tensor of a call: a contiguous CUDA tensor on `device`."""
-    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
         return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
@@ -344,23 +344,28 @@ def _want(t, name, dtypes, shape, device):
 def _on_device(device, stream, body):
     """body(raw stream) with `device` current, and, where a stream is given, that stream too: what body allocates
     then belongs to the stream that uses it."""
-    torch = _torch()
-    if stream is not None:
+    if stream is None:
+        torch = _torch()
+        index = device.index
+        if torch.cuda.current_device() == index:
+            return body(_raw_stream(index))
+        with torch.cuda.device(device):
+            return body(_raw_stream(index))
+    else:
+        torch = _torch()
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             return body(stream.cuda_stream)
-    if torch.cuda.current_device() == device.index:
-        return body(_raw_stream(device.index))
-    with torch.cuda.device(device):
-        return body(_raw_stream(device.index))
 
 
 def _raw_stream(index):
     """The current stream of a device (torch's own call for it where there is one: a third of a step's host time else)."""
     torch = _torch()
-    quick = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return quick(index) if quick else torch.cuda.current_stream(index).cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 _SPARE = {}
@@ -509,11 +514,11 @@ def _rows(t, name, heads, d, tokens, device):
     """Checks a [T, heads, d] bf16 tensor whose tokens may lie further apart than their heads fill (a slice of a fused
     projection) and returns the distance in elements."""
     torch = _torch()
-    if not t.is_cuda or t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must have shape {(tokens, heads, d)}, got {tuple(t.shape)}")
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != d):
@@ -525,13 +530,15 @@ def _cache(cu_seqlens, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale,
     torch = _torch()
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must have 4 dims, block_table 2")
-    pages, h_kv, page, d = k_cache.shape
-    _want(kv_lens, "kv_lens", (torch.int32,), (n,), device)
-    _want(block_table, "block_table", (torch.int32,), (n, block_table.shape[1]), device)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _want(t, name, (torch.float8_e4m3fn, torch.uint8), (pages, h_kv, page, d), device)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _want(t, name, (torch.float32,), (pages, h_kv), device)
+    cache, scales = k_cache.shape, k_cache.shape[:2]
+    pages, h_kv, page, d = cache
+    i32, f32, e4m3 = (torch.int32,), (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
+    _want(kv_lens, "kv_lens", i32, (n,), device)
+    _want(block_table, "block_table", i32, (n, block_table.shape[1]), device)
+    _want(k_cache, "k_cache", e4m3, cache, device)
+    _want(v_cache, "v_cache", e4m3, cache, device)
+    _want(k_scale, "k_scale", f32, scales, device)
+    _want(v_scale, "v_scale", f32, scales, device)
     return pages, h_kv, page, d
 
 
