@@ -380,16 +380,192 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(lo_at + at), "l"(src + 4), "r"(bytes) : "memory");
             }
         };
-        bool more = line.next(seg);
-        if (more) fetch_queries(seg);
-        for (int unit = 0; alive && more; ++unit) {
-            const int tiles = seg.b1 - seg.b0;
+        // The fetched queries as hi + lo; the row's factor.
+        auto split_queries = [&]() {
+            float *scales = misc.row_scale[q_tile];
+            const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
+            asm volatile("cp.async.wait_all;\n" ::: "memory");
+#pragma unroll 4
+            for (int i = sub; i < kMine; i += kAtOnce) {
+                const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
+                const uint2 a = lds64(hi_at + at), b = lds64(lo_at + at);
+                const uint32_t x[4] = {a.x, a.y, b.x, b.y};
+                float f[8], top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
+                    top = fmaxf(top, fabsf(f[e]));
+                }
+#pragma unroll
+                for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float down = row_down(top), factor = down * sign;
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
+                    hi[e] = clipped_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
+                    lo[e] = clipped_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
+                }
+                sts64(hi_at + at, hi[0], hi[1]);
+                sts64(lo_at + at, lo[0], lo[1]);
+                // the inverse of a power of two, by its exponent; every lane of the row writes the same.  An infinity,
+                // which the conversion clips, spoils its row here (a NaN does so as a NaN).
+                const float one = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
+                scales[row0 + i] = top <= 3.402823466e38f ? one : __uint_as_float(0x7fc00000u);
+            }
+            tc::fence_async_smem();
+            tc::mbar_arrive(&misc.q_full);
+            if (kSplit) named_sync(bar_id, bar_count); else __syncwarp();
+            return scales[row];
+        };
+        // Of a unit: what is left to do once its products are issued, while the next unit's begin.
+        int tiles = 0, last = 0, token = 0, head = 0, seen = 0;
+        bool real = false;
+        float m = kNone, l = 0.f, row_scale = 0.f;
+        auto finish = [&]() {
+            if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
+                float(*sums)[128] = misc.top[(last + 1) & 1];
+                sums[group][row] = l;
+                named_sync(bar_id, bar_count);
+                l = sums[0][row] + sums[1][row];
+            }
+            if (tiles > 0 && !wait(misc.pv_done[last & 1], last >> 1)) return;
+            tc::tc_fence_after();
+
+            // ---- the unit's sums
+            const int first_cta = seg.whole ? 0 : line.first_cta(seg), last_cta = seg.whole ? 0 : line.last_cta(seg);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const long long out_row = (long long)(seg.bos + token) * p.h_q + head;
+            const int slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
+            // outputs: a warp's 32 rows by 32 columns through shared memory, so that four lanes write a row's 64 bytes
+            uint8_t *staging = smem + S::off_staging + warp * 32 * S::kPitch;
+            long long to[4];  // where rows lane / 4 + 8 i go, or -1
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                to[i] = __shfl_sync(0xffffffffu, real && !bad_pages ? out_row : -1ll, (lane >> 2) + 8 * i);
+                if (to[i] >= 0) to[i] = to[i] * D + out0 + (lane & 3) * 8;
+            }
+            // part sums: [slot][tile][D / 4][128 rows] of four columns, so that neighbouring rows lie together
+            float4 *part = reinterpret_cast<float4 *>(p.parts) + ((long long)(slot * NQ + q_tile) * D + out0) / 4 * 128 + row;
+            const bool poisoned = tiles > 0 && misc.poison[filled % kPoisonSlots] == filled + 1;
+            filled += tiles > 0;
+            const int edge0 = line_seen(p, seg, 0, S::kRows) / kHalf * kHalf;  // the first stage that rows see differently
+#pragma unroll 1
+            for (int c = 0; c < kOut; c += 32) {
+                uint32_t y[32];
+                if (tiles > 0) {
+                    tc::tmem_ld_32x32b_x32(o_at + c, y);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = 0;
+                }
+                if (poisoned && real && !bad_pages) {
+                    const uint32_t hit = nan_columns(p, seg, max(edge0, seg.b0 * kTok), min(seen, seg.b1 * kTok), out0 + c, D);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = hit >> e & 1 ? 0x7fc00000u : y[e];
+                }
+                if (seg.whole) {
+                    const uint32_t mine = tc::smem_u32(staging) + lane * S::kPitch;
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        sts128(mine + e * 2, pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
+                               pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (lane & 3) * 16);
+                        if (to[i] >= 0) *reinterpret_cast<uint4 *>(p.o + to[i] + c) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        part[(c + e) / 4 * 128] = make_float4(__uint_as_float(y[e]), __uint_as_float(y[e + 1]),
+                                                              __uint_as_float(y[e + 2]), __uint_as_float(y[e + 3]));
+                }
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(&misc.o_free);
+            if (seg.whole) {
+                if (real && !bad_pages && p.lse && out0 == 0) p.lse[out_row] = log_sum(m, l);
+            } else {
+                if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
+                named_sync(bar_id, bar_count);
+                if (row == 0 && out0 == 0) {
+                    int *ticket = &p.tickets[first_cta * NQ + q_tile];
+                    const bool mine = take_ticket(ticket) == last_cta - first_cta;
+                    if (mine) *ticket = 0;
+                    misc.ticket[q_tile] = mine;
+                }
+                named_sync(bar_id, bar_count);
+                if (misc.ticket[q_tile] && real && !bad_pages) {
+                    const int parts = last_cta - first_cta + 1;
+                    auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
+                    float M = kNone, L = 0.f;
+#pragma unroll 1
+                    for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
+#pragma unroll 1
+                    for (int i = 0; i < parts; ++i) {
+                        const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
+                        L = fmaf(ml.y, exp2f(ml.x - M), L);
+                    }
+                    const float one = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+                    for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
+                        float4 sum[8] = {};
+#pragma unroll 1
+                        for (int i = 0; i < parts; ++i) {
+                            const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
+                            const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = __ldcg(src + e * 128);
+                                sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
+                                sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2)
+                            *reinterpret_cast<uint4 *>(p.o + out_row * D + 4 * (c + e)) =
+                                make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
+                                           pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
+                                           pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
+                    }
+                    if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
+                }
+                named_sync(bar_id, bar_count);  // the ticket may be written again
+            }
+        };
+        Segment next;
+        bool more = line.next(next), have = false;  // the unit after: found early, or late where units are long
+        while (alive) {
+            // Every product with the last unit's queries is done.  The next one's come first, so that its scores are
+            // formed while the last one's sums are written; where those go out by way of the queries' place, after them.
+            if (kSplit && have) {
+                finish();
+                named_sync(bar_id, bar_count);
+                more = line.next(next);
+            }
+            if (more) {
+                fetch_queries(next);
+                row_scale = split_queries();
+            }
+            if (!kSplit && have) finish();
+            if (!more || !alive) break;
+            seg = next;
+            if (!kSplit) more = line.next(next);
+            have = true;
+            tiles = seg.b1 - seg.b0;
             const int g0 = seg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
             const int r = q_tile * 128 + row;
-            int token, head;
             place(seg, token0, head0, r, token, head);
-            const bool real = r < seg.rows && SR_IN_BOUNDS(seg.bos + token, p.total, p.status);
-            const int seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
+            real = r < seg.rows && SR_IN_BOUNDS(seg.bos + token, p.total, p.status);
+            seen = real ? max(0, seg.kv - seg.count + token + 1) : 0;
             if (checked != seg.seq) {
                 bool bad = false;
                 const int pages = (seg.kv + p.page - 1) >> p.page_shift;
@@ -402,49 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bad_pages && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
                 checked = seg.seq;
             }
-            // the queries as hi + lo
-            float row_scale;
-            {
-                float *scales = misc.row_scale[q_tile];
-                const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
-                asm volatile("cp.async.wait_all;\n" ::: "memory");
-#pragma unroll 4
-                for (int i = sub; i < kMine; i += kAtOnce) {
-                    const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
-                    const uint2 a = lds64(hi_at + at), b = lds64(lo_at + at);
-                    const uint32_t x[4] = {a.x, a.y, b.x, b.y};
-                    float f[8], top = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
-                        top = fmaxf(top, fabsf(f[e]));
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float down = row_down(top), factor = down * sign;
-                    uint32_t hi[2], lo[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) f[4 * e + k] *= factor;
-                        hi[e] = clipped_e4m3x4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                        const float2 u = e4m3x2_to_float2(hi[e]), v = e4m3x2_to_float2(hi[e] >> 16);
-                        lo[e] = clipped_e4m3x4(f[4 * e] - u.x, f[4 * e + 1] - u.y, f[4 * e + 2] - v.x, f[4 * e + 3] - v.y);
-                    }
-                    sts64(hi_at + at, hi[0], hi[1]);
-                    sts64(lo_at + at, lo[0], lo[1]);
-                    // the inverse of a power of two, by its exponent; every lane of the row writes the same.  An infinity,
-                    // which the conversion clips, spoils its row here (a NaN does so as a NaN).
-                    const float one = fabsf(p.scale_log2) * (1.f / 256.f) * __uint_as_float((254u << 23) - __float_as_uint(down));
-                    scales[row0 + i] = top <= 3.402823466e38f ? one : __uint_as_float(0x7fc00000u);
-                }
-                tc::fence_async_smem();
-                tc::mbar_arrive(&misc.q_full);
-                if (kSplit) named_sync(bar_id, bar_count); else __syncwarp();
-                row_scale = scales[row];
-            }
-
-            float m = kNone, l = 0.f;
+            m = kNone, l = 0.f;
             // Lane g of every eight (four) holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
             // columns, loaded a tile ahead, their page two.
             auto page_of = [&](int b) {
@@ -555,136 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tc_fence_before();
                 tc::mbar_arrive(&misc.p_full[buf]);
             }
-            const int last = w + (tiles - 1) * NQ + q_tile;
+            last = w + (tiles - 1) * NQ + q_tile;
             w += tiles * NQ;
-            if (!alive) break;
-            // the next unit's queries: every product with this one's is done
-            Segment next;
-            if (!kSplit) {
-                more = line.next(next);
-                if (more) fetch_queries(next);
-            }
-            if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
-                float(*sums)[128] = misc.top[(last + 1) & 1];
-                sums[group][row] = l;
-                named_sync(bar_id, bar_count);
-                l = sums[0][row] + sums[1][row];
-            }
-            if (tiles > 0 && !wait(misc.pv_done[last & 1], last >> 1)) break;
-            tc::tc_fence_after();
-
-            // ---- the unit's sums
-            const int first_cta = seg.whole ? 0 : line.first_cta(seg), last_cta = seg.whole ? 0 : line.last_cta(seg);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long out_row = (long long)(seg.bos + token) * p.h_q + head;
-            const int slot = 2 * blockIdx.x + (int(blockIdx.x) == first_cta ? 1 : 0);
-            // outputs: a warp's 32 rows by 32 columns through shared memory, so that four lanes write a row's 64 bytes
-            uint8_t *staging = smem + S::off_staging + warp * 32 * S::kPitch;
-            long long to[4];  // where rows lane / 4 + 8 i go, or -1
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                to[i] = __shfl_sync(0xffffffffu, real && !bad_pages ? out_row : -1ll, (lane >> 2) + 8 * i);
-                if (to[i] >= 0) to[i] = to[i] * D + out0 + (lane & 3) * 8;
-            }
-            // part sums: [slot][tile][D / 4][128 rows] of four columns, so that neighbouring rows lie together
-            float4 *part = reinterpret_cast<float4 *>(p.parts) + ((long long)(slot * NQ + q_tile) * D + out0) / 4 * 128 + row;
-            const bool poisoned = tiles > 0 && misc.poison[filled % kPoisonSlots] == filled + 1;
-            filled += tiles > 0;
-            const int edge0 = line_seen(p, seg, 0, S::kRows) / kHalf * kHalf;  // the first stage that rows see differently
-#pragma unroll 1
-            for (int c = 0; c < kOut; c += 32) {
-                uint32_t y[32];
-                if (tiles > 0) {
-                    tc::tmem_ld_32x32b_x32(o_at + c, y);
-                    tc::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = 0;
-                }
-                if (poisoned && real && !bad_pages) {
-                    const uint32_t hit = nan_columns(p, seg, max(edge0, seg.b0 * kTok), min(seen, seg.b1 * kTok), out0 + c, D);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = hit >> e & 1 ? 0x7fc00000u : y[e];
-                }
-                if (seg.whole) {
-                    const uint32_t mine = tc::smem_u32(staging) + lane * S::kPitch;
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        sts128(mine + e * 2, pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
-                               pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
-                               pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
-                               pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (lane & 3) * 16);
-                        if (to[i] >= 0) *reinterpret_cast<uint4 *>(p.o + to[i] + c) = v;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        part[(c + e) / 4 * 128] = make_float4(__uint_as_float(y[e]), __uint_as_float(y[e + 1]),
-                                                              __uint_as_float(y[e + 2]), __uint_as_float(y[e + 3]));
-                }
-            }
-            tc::tc_fence_before();
-            tc::mbar_arrive(&misc.o_free);
-            if (seg.whole) {
-                if (real && !bad_pages && p.lse && out0 == 0) p.lse[out_row] = log_sum(m, l);
-            } else {
-                if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
-                named_sync(bar_id, bar_count);
-                if (row == 0 && out0 == 0) {
-                    int *ticket = &p.tickets[first_cta * NQ + q_tile];
-                    const bool mine = take_ticket(ticket) == last_cta - first_cta;
-                    if (mine) *ticket = 0;
-                    misc.ticket[q_tile] = mine;
-                }
-                named_sync(bar_id, bar_count);
-                if (misc.ticket[q_tile] && real && !bad_pages) {
-                    const int parts = last_cta - first_cta + 1;
-                    auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
-                    float M = kNone, L = 0.f;
-#pragma unroll 1
-                    for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
-#pragma unroll 1
-                    for (int i = 0; i < parts; ++i) {
-                        const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
-                        L = fmaf(ml.y, exp2f(ml.x - M), L);
-                    }
-                    const float one = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll 1
-                    for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
-                        float4 sum[8] = {};
-#pragma unroll 1
-                        for (int i = 0; i < parts; ++i) {
-                            const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
-                            const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 v = __ldcg(src + e * 128);
-                                sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
-                                sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2)
-                            *reinterpret_cast<uint4 *>(p.o + out_row * D + 4 * (c + e)) =
-                                make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
-                                           pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
-                                           pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
-                    }
-                    if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
-                }
-                named_sync(bar_id, bar_count);  // the ticket may be written again
-            }
-            if (kSplit) {
-                named_sync(bar_id, bar_count);  // the staging is the queries' again
-                more = line.next(next);
-                if (more) fetch_queries(next);
-            }
-            seg = next;
         }
     }
 done:
