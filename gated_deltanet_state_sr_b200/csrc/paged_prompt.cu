@@ -24,8 +24,6 @@
 //   a warp that loads pages of keys, and one for values.
 // Tensor memory: two buffers of scores (128 columns each) and the sums O (two
 // times 128 columns, or 256).
-#include <type_traits>
-
 #include "paged_attention.cuh"
 
 namespace sr {
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto fetch_queries = [&](const Segment &sg) {
             const int g0 = sg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = sub; i < kMine; i += kAtOnce) {
                 const int x = q_tile * 128 + row0 + i;
                 int tx, hx;
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *scales = misc.row_scale[q_tile];
             const float sign = p.scale_log2 < 0.f ? -256.f : 256.f;  // a score's factor is not negative
             asm volatile("cp.async.wait_all;\n" ::: "memory");
-#pragma unroll 4
+#pragma unroll 2
             for (int i = sub; i < kMine; i += kAtOnce) {
                 const uint32_t at = chunk8_at<D>(128, row0 + i, c8 >> 1) + (c8 & 1) * 8;
                 const uint2 a = lds64(hi_at + at), b = lds64(lo_at + at);
@@ -613,9 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t y[32];
                     tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
                     tc::tmem_ld_wait();
-                    if (edge)
+                    if (edge) {  // -inf where the row does not see, also for the second pass
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) y[c] = tok0 + 32 * q + c < seen ? y[c] : 0xff800000u;  // -inf
+                        for (int c = 0; c < 32; ++c) y[c] = tok0 + 32 * q + c < seen ? y[c] : 0xff800000u;
+                        tc::tmem_st_32x32b_x32(s_at + 32 * q, y);
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float most[2] = {__uint_as_float(y[16 * h]), __uint_as_float(y[16 * h + 1])};
@@ -625,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = fmaxf(top, fmaf(fmaxf(most[0], most[1]), k, __shfl_sync(0xffffffffu, lv, 2 * q + h)));
                     }
                 }
+                if (edge) tc::tmem_st_wait();
                 if (kSplit) {  // the other half's largest
                     misc.top[buf][group][row] = top;
                     named_sync(bar_id, bar_count);
@@ -649,8 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float z = m - kShift;
                 // weights of columns 32 q .., over 16 columns of the scores' own, all of them read already
-                auto weights_of = [&](const uint32_t(&y)[32], int q, auto masked) {
-                    uint32_t out[16];
+#pragma unroll 1
+                for (int q = 0; q < kChunks; ++q) {
+                    uint32_t y[32], out[16];
+                    tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
+                    tc::tmem_ld_wait();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float k = row_scale * __shfl_sync(0xffffffffu, ks, 2 * q + h);
@@ -658,33 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float sum[2] = {0.f, 0.f};
 #pragma unroll
                         for (int c = 16 * h; c < 16 * h + 16; c += 2) {
-                            float a = ex2(fmaf(__uint_as_float(y[c]), k, v));
-                            float b = ex2(fmaf(__uint_as_float(y[c + 1]), k, v));
-                            if (masked) {
-                                a = tok0 + 32 * q + c < seen ? a : 0.f;
-                                b = tok0 + 32 * q + c + 1 < seen ? b : 0.f;
-                            }
+                            const float a = ex2(fmaf(__uint_as_float(y[c]), k, v));
+                            const float b = ex2(fmaf(__uint_as_float(y[c + 1]), k, v));
                             sum[0] += a, sum[1] += b;
                             out[c / 2] = pack_f16(a, b);
                         }
                         l = fmaf(sum[0] + sum[1], __shfl_sync(0xffffffffu, up, 2 * q + h), l);
                     }
                     tc::tmem_st_32x32b_x16(s_at + 16 * q, out);
-                };
-                auto weights = [&](auto masked) {
-#pragma unroll 1
-                    for (int q = 0; q < kChunks; ++q) {
-                        uint32_t y[32];
-                        tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
-                        tc::tmem_ld_wait();
-                        weights_of(y, q, masked);
-                    }
-                };
-                // two copies: with the test in the loop every pair of columns would be a block of its own
-                if (edge)
-                    weights(std::true_type{});
-                else
-                    weights(std::false_type{});
+                }
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&misc.p_full[buf]);
