@@ -17,7 +17,10 @@
 // position of 10^6 times 1 rad leaves fp32 no fraction) costs more than the
 // rotation itself.  A warp takes one head of the page: keys and values in two
 // passes over the bf16 rows, the first for the largest magnitude, the second
-// from the caches that the first filled.
+// from the caches that the first filled.  Measured: 8917 new tokens of eight
+// requests, 32 + 8 heads of 128, positions on three axes, 55 us (3.8 TB/s on the
+// bytes that have to move); one token for each of 64 requests, 16 + 4 heads of
+// 256, 6 us a call in a captured graph.
 #include <type_traits>
 
 #include "paged.cuh"

@@ -10,7 +10,11 @@
 // and reads a_t, dy_t and the stored h_{t-1} of one row each.
 //
 // Both are bound by memory: forward moves x, g in and y out, backward g, dy, y
-// in and dx, dg out, each once.
+// in and dx, dg out, each once.  Measured (cold L2): 32768 tokens x 2560 channels
+// in fp32 186 us, 5.4 TB/s; its gradients with bf16 rows and fp32 gates 221 us,
+// 5.3 TB/s; eight sequences of 512 to 2048 tokens x 4096 channels (bf16, fp32
+// gates) 65 us, 4.6 TB/s, their gradients 78 us.  What is left there is the last
+// wave of CTAs; a single long sequence is held by the exchange between waves.
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -97,7 +101,8 @@ __device__ __forceinline__ float step(float a, float b, float h) {
 __device__ __forceinline__ float decay(float g) { return expf(g); }
 
 // Sequences of a few tokens (a decode step is one): a thread walks one
-// sequence of VEC channels.  No exchange between threads.
+// sequence of VEC channels.  No exchange between threads.  64 x 2560: 4 us a call
+// in a captured graph, the clearing of the status word included.
 template <typename XT, typename GT, int VEC, bool BWD>
 __global__ void __launch_bounds__(128) linrec_short(LinrecParams p) {
     const int c0 = (blockIdx.x * 128 + threadIdx.x) * VEC;
@@ -327,8 +332,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) linrec_scan(LinrecParams p) {
 }
 
 // The same walk with the rows brought by TMA, 64 tokens by 64 channels at a time, into a ring of stages: what a memory
-// this fast needs in flight (200 KB an SM here) is more than registers hold.  For rows whose size is a multiple of 16
-// bytes, at an address that is.
+// this fast needs in flight (200 KB an SM here) is more than registers hold (82 us for the eight sequences above with
+// loads into registers, 65 so).  For rows whose size is a multiple of 16 bytes, at an address that is.
 template <typename XT, typename GT, bool BWD> struct TmaShape {
     static constexpr int kTok = kWarps * kSteps, kCols = 64;
     static constexpr int kX = kTok * kCols * int(sizeof(XT)), kG = kTok * kCols * int(sizeof(GT));
@@ -452,7 +457,8 @@ __global__ void __launch_bounds__(kWarps * 32, TmaShape<XT, GT, BWD>::kPerSm)
 constexpr int kShortLen = 8;
 
 // A sequence's column block is spread over as many CTAs as the GPU holds at once, while each still has a wave of tokens
-// of its own: a cluster that has to wait for room would start when the others are done.
+// of its own: a cluster that has to wait for room would start when the others are done (32768 x 2560 in fp32: clusters
+// of four 248 us, of six, the largest that fit at once, 186 us, of seven 277 us).
 template <typename K> int cluster_size(K kernel, cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, long long units, int max_len) {
     for (int C = kMaxCluster; C > 1; --C) {
         if ((C - 1) * kWarps * kSteps >= max_len) continue;

@@ -32,6 +32,12 @@
 // stages (128-byte swizzle, which makes every fragment load below free of bank
 // conflicts), and groups of four warps that take the stages in turn, 16 tokens a
 // warp, with softmax state of their own; they are joined once per unit.
+//
+// Measured: one token for each of eight requests with 30K to 32K cached (32 / 8
+// heads of 128, 522 MB) 107 us back to back, 4.9 TB/s; for each of 64 requests
+// with 256 to 4096 (16 / 4 heads of 256, 315 MB) 68 us, 4.6 TB/s; one token over
+// 820 cached 16 us, which is latency: finding its part of the work, queries, one
+// stage, joining the warps and then the CTAs.
 #include "paged_attention.cuh"
 
 namespace sr {
@@ -40,7 +46,9 @@ namespace {
 
 constexpr int kTok = 64;               // tokens per stage: 4 warps of 16
 constexpr int kMinBlocks = 2;          // least blocks worth a CTA of their own
-constexpr int kUnitStart = 512;        // what a unit costs beside its blocks, in tokens
+// What a unit costs beside its blocks, in tokens: the 64 ragged requests above took 77 us with 128, 76 with 256, 70 with
+// 512.
+constexpr int kUnitStart = 512;
 
 // Consumer warps by what a lane has to hold: D / 4 sums for every eight queries, D / 8 bytes of values, fragments.
 template <int D, int NT> struct RowsShape {

@@ -14,6 +14,10 @@ Contents
                      schedule in numpy fp64 (``oracle/layers.py``).
 * ``planning``       checkpoint placement: the objective, exhaustive search
                      and the literal recurrence (``oracle/planning.py``).
+* ``linrec``         the elementwise gated linear recurrence and its gradients
+                     in numpy fp64 (``oracle/linrec.py``).
+* ``paged``          rotation, append and attention of the paged 8-bit cache in
+                     numpy fp64 (``oracle/paged.py``).
 
 Parity status of each function (what pins it, see ``tests/test_oracle_*``):
 * gdn_replay / mamba2_replay: pinned by closed forms (beta = 0 decay,
