@@ -15,6 +15,8 @@
 // 5.3 TB/s; eight sequences of 512 to 2048 tokens x 4096 channels (bf16, fp32
 // gates) 65 us, 4.6 TB/s, their gradients 78 us.  What is left there is the last
 // wave of CTAs; a single long sequence is held by the exchange between waves.
+#include <math.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -100,11 +102,13 @@ __device__ __forceinline__ float step(float a, float b, float h) {
 // of g) would add up to 1e-4 at a memory of a thousand tokens.
 __device__ __forceinline__ float decay(float g) { return expf(g); }
 
-// Sequences of a few tokens (a decode step is one): a thread walks one
-// sequence of VEC channels.  No exchange between threads.  64 x 2560: 4 us a call
-// in a captured graph, the clearing of the status word included.
+// A thread walks one sequence of VEC channels, with no exchange between threads: for sequences of a few tokens (a
+// decode step is one; 64 x 2560 take 4 us a call in a captured graph, the clearing of the status word included), and
+// wherever there are so many that the walk's latency is hidden.  Eight tokens' rows are loaded before the first is
+// walked, since a load cannot pass a store that might be to the same place.
 template <typename XT, typename GT, int VEC, bool BWD>
 __global__ void __launch_bounds__(128) linrec_short(LinrecParams p) {
+    constexpr int kBatch = 8;
     const int c0 = (blockIdx.x * 128 + threadIdx.x) * VEC;
     const int seq = blockIdx.y;
     if (c0 >= p.D) return;
@@ -116,29 +120,38 @@ __global__ void __launch_bounds__(128) linrec_short(LinrecParams p) {
     load_state<VEC>(BWD ? p.ds : p.h0, soff, nst, p.status, h);
     if (BWD) load_state<VEC>(p.h0, soff, nst, p.status, h0);
     const int len = eos - bos;
-#pragma unroll 4
-    for (int i = 0; i < len; ++i) {
-        const int t = BWD ? eos - 1 - i : bos + i;
-        const long long off = (long long)t * p.D + c0;
-        float a[VEC], b[VEC], prev[VEC], o[VEC];
-        Vec<GT, VEC>::get(load_row<GT, VEC>(p.g, off, nel, p.status), a);
-        Vec<XT, VEC>::get(load_row<XT, VEC>(p.in, off, nel, p.status), b);
-        if (BWD) {
-            if (t > bos)
-                Vec<XT, VEC>::get(load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status), prev);
-            else
+#pragma unroll 1
+    for (int base = 0; base < len; base += kBatch) {
+        typename Vec<GT, VEC>::Raw rg[kBatch];
+        typename Vec<XT, VEC>::Raw rx[kBatch], ry[kBatch];
 #pragma unroll
-                for (int c = 0; c < VEC; ++c) prev[c] = h0[c];
+        for (int i = 0; i < kBatch; ++i) {
+            const int t = BWD ? eos - 1 - base - i : bos + base + i;
+            const long long off = (long long)t * p.D + c0;
+            if (base + i < len) rg[i] = load_row<GT, VEC>(p.g, off, nel, p.status);
+            if (base + i < len) rx[i] = load_row<XT, VEC>(p.in, off, nel, p.status);
+            if (BWD && base + i < len - 1) ry[i] = load_row<XT, VEC>(p.y_in, off - p.D, nel, p.status);
         }
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            if (BWD) o[c] = b[c] + h[c];
-            h[c] = step<BWD>(decay(a[c]), b[c], h[c]);
-            if (!BWD) o[c] = h[c];
-            if (BWD) prev[c] *= h[c];
+        for (int i = 0; i < kBatch; ++i) {
+            if (base + i >= len) break;
+            const int t = BWD ? eos - 1 - base - i : bos + base + i;
+            const long long off = (long long)t * p.D + c0;
+            float a[VEC], b[VEC], prev[VEC], o[VEC];
+            Vec<GT, VEC>::get(rg[i], a);
+            Vec<XT, VEC>::get(rx[i], b);
+            if (BWD) Vec<XT, VEC>::get(ry[i], prev);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                if (BWD) prev[c] = base + i < len - 1 ? prev[c] : h0[c];
+                if (BWD) o[c] = b[c] + h[c];
+                h[c] = step<BWD>(decay(a[c]), b[c], h[c]);
+                if (!BWD) o[c] = h[c];
+                if (BWD) prev[c] *= h[c];
+            }
+            if (BWD) store_row<GT, VEC>(p.dg, off, nel, p.status, prev);
+            if (p.out) store_row<XT, VEC>(p.out, off, nel, p.status, o);
         }
-        if (BWD) store_row<GT, VEC>(p.dg, off, nel, p.status, prev);
-        if (p.out) store_row<XT, VEC>(p.out, off, nel, p.status, o);
     }
     if (p.last)
 #pragma unroll
@@ -453,15 +466,28 @@ __global__ void __launch_bounds__(kWarps * 32, TmaShape<XT, GT, BWD>::kPerSm)
             if (SR_IN_BOUNDS(soff + c, nst, p.status)) p.last[soff + c] = carry[c];
 }
 
-// A sequence of at most this many tokens is walked by one thread per channel pair.
-constexpr int kShortLen = 8;
+// Whether threads that walk a sequence each do a call sooner than CTAs that share one out.  A walk takes 0.11 us a token
+// (0.22 backward); sharing takes a CTA 0.7 us and 1.6 a wave of 64 tokens, 296 of them at a time, and a sequence's
+// cluster 4 us and 1.4 a wave; neither is faster than memory.  Measured (forward us, walked and shared): 1000 sequences
+// of 20 tokens x 2560 channels 72 and 361, of 200 tokens 628 and 946; 256 of 100 x 1000 40 and 141; 64 of 500 x 2560 119
+// and 125, 64 of 40 10 and 31, 8 of 20 6 and 8; but 8 of 60 x 512 8 and 6, one of 64 x 2560 8 and 6.
+bool walked(const LinrecParams &p, int bytes, bool backward) {
+    const double memory = double(p.total) * p.D * bytes / 6.2e6, walk = (backward ? 0.22 : 0.11) * p.max_len;
+    const double blocks = (p.D + 63) / 64, units = blocks * p.n_seqs;
+    const double waves = (p.max_len + kWarps * kSteps - 1) / (kWarps * kSteps);
+    const double C = fmin(fmin(fmax(floor(296 / units), 1.0), double(kMaxCluster)), fmax(waves, 1.0));
+    const double shared = fmax(blocks * (0.7 * p.n_seqs + 1.6 * (p.total / 64.0 + p.n_seqs)) / 296, 4 + 1.4 * waves / C);
+    return fmax(memory, walk) < fmax(memory, shared);
+}
 
 // A sequence's column block is spread over as many CTAs as the GPU holds at once, while each still has a wave of tokens
 // of its own: a cluster that has to wait for room would start when the others are done (32768 x 2560 in fp32: clusters
 // of four 248 us, of six, the largest that fit at once, 186 us, of seven 277 us).
 template <typename K> int cluster_size(K kernel, cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, long long units, int max_len) {
-    for (int C = kMaxCluster; C > 1; --C) {
-        if ((C - 1) * kWarps * kSteps >= max_len) continue;
+    // no more than two CTAs an SM, and no CTA without tokens: seldom more than two sizes are left to ask for
+    const long long most = 2 * 148 / units, waves = (max_len + kWarps * kSteps - 1) / (kWarps * kSteps);
+    const long long bound = most < waves ? most : waves;
+    for (int C = bound < kMaxCluster ? int(bound) : kMaxCluster; C > 1; --C) {
         at->val.clusterDim.x = C;
         cfg.gridDim.x = C;  // what the query looks at is the cluster
         int fit = 0;
@@ -490,8 +516,8 @@ template <typename K> void set_grid(cudaLaunchConfig_t &cfg, cudaLaunchAttribute
 }
 
 template <typename XT, typename GT, int VEC, bool BWD>
-cudaError_t launch(LinrecParams p, cudaStream_t st) {
-    if (p.max_len <= kShortLen) {
+cudaError_t launch(LinrecParams p, bool walk, cudaStream_t st) {
+    if (walk) {
         const int per = 128 * VEC;
         linrec_short<XT, GT, VEC, BWD><<<dim3((p.D + per - 1) / per, p.n_seqs), 128, 0, st>>>(p);
         return cudaGetLastError();
@@ -530,10 +556,11 @@ cudaError_t pick(const LinrecParams &p, cudaStream_t st) {
     const bool two = rows(p.in, sizeof(XT), 2 * sizeof(XT)) && rows(p.g, sizeof(GT), 2 * sizeof(GT)) &&
                      rows(p.y_in, sizeof(XT), 2 * sizeof(XT)) && rows(p.out, sizeof(XT), 2 * sizeof(XT)) &&
                      rows(p.dg, sizeof(GT), 2 * sizeof(GT));
-    if (!two) return launch<XT, GT, 1, BWD>(p, st);
-    if (p.max_len > kShortLen && rows(p.in, sizeof(XT), 16) && rows(p.g, sizeof(GT), 16) && rows(p.y_in, sizeof(XT), 16))
+    const bool walk = walked(p, BWD ? 3 * sizeof(XT) + 2 * sizeof(GT) : 2 * sizeof(XT) + sizeof(GT), BWD);
+    if (!two) return launch<XT, GT, 1, BWD>(p, walk, st);
+    if (!walk && rows(p.in, sizeof(XT), 16) && rows(p.g, sizeof(GT), 16) && rows(p.y_in, sizeof(XT), 16))
         return launch_tma<XT, GT, BWD>(p, st);
-    return launch<XT, GT, 2, BWD>(p, st);
+    return launch<XT, GT, 2, BWD>(p, walk, st);
 }
 
 template <bool BWD>

@@ -114,6 +114,15 @@ def test_many_sequences(sr):
     check_backward(sr, c, y)
 
 
+def test_many_short_sequences_beside_a_long_one(sr):
+    lens = [(5 * i) % 7 for i in range(299)]
+    lens.insert(150, 2500)
+    for D in (64, 37):
+        c = make(lens, D, BF, BF, seed=14)
+        y, _ = check_forward(sr, c)
+        check_backward(sr, c, y)
+
+
 def test_unaligned_rows_take_single_channels(sr):
     """Rows whose pairs of channels straddle the alignment: a view that starts one element into its storage."""
     c = make([33, 70], 6, BF, BF, seed=5)
