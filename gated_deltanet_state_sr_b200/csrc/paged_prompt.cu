@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (lane & 3) * 16);
                         if (to[i] >= 0) *reinterpret_cast<uint4 *>(p.o + to[i] + c) = v;
                     }
-                } else {
+                } else if (real) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         part[(c + e) / 4 * 128] = make_float4(__uint_as_float(y[e]), __uint_as_float(y[e + 1]),
@@ -511,40 +511,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     misc.ticket[q_tile] = mine;
                 }
                 named_sync(bar_id, bar_count);
-                if (misc.ticket[q_tile] && real && !bad_pages) {
+                const int mine = min(128, seg.rows - q_tile * 128);  // rows of the tile that there are
+                if (misc.ticket[q_tile] && mine > 0 && !bad_pages) {
                     const int parts = last_cta - first_cta + 1;
                     auto at = [&](int i) { return (2 * (first_cta + i) + (i == 0)) * NQ + q_tile; };
-                    float M = kNone, L = 0.f;
-#pragma unroll 1
-                    for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + row]).x);
-#pragma unroll 1
-                    for (int i = 0; i < parts; ++i) {
-                        const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + row]);
-                        L = fmaf(ml.y, exp2f(ml.x - M), L);
-                    }
-                    const float one = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll 1
-                    for (int c = out0 / 4; c < (out0 + kOut) / 4; c += 8) {
-                        float4 sum[8] = {};
-#pragma unroll 1
+                    // a row to every thread, or, where there are few, to several, which share its columns out
+                    const int shift = 32 - __clz(mine - 1), of = row & ((1 << shift) - 1);
+                    const int g = seg.tile * S::kRows + q_tile * 128 + of;
+                    const long long to_row = (long long)(seg.bos + g / p.group) * p.h_q + seg.head * p.group + g % p.group;
+                    if (of < mine) {
+                        float M = kNone, L = 0.f;
+#pragma unroll 2
+                        for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(&p.part_ml[at(i) * 128 + of]).x);
+#pragma unroll 2
                         for (int i = 0; i < parts; ++i) {
-                            const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + row]).x - M);
-                            const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((long long)at(i) * (D / 4) + c) * 128 + row;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 v = __ldcg(src + e * 128);
-                                sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
-                                sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
-                            }
+                            const float2 ml = __ldcg(&p.part_ml[at(i) * 128 + of]);
+                            L = fmaf(ml.y, exp2f(ml.x - M), L);
                         }
+                        const float one = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+                        for (int c = (row >> shift) * 4; c < kOut / 4; c += (128 >> shift) * 4) {
+                            float4 sum[4] = {};
+#pragma unroll 2
+                            for (int i = 0; i < parts; ++i) {
+                                const float f = exp2f(__ldcg(&p.part_ml[at(i) * 128 + of]).x - M);
+                                const float4 *src = reinterpret_cast<const float4 *>(p.parts) +
+                                                    ((long long)at(i) * (D / 4) + out0 / 4 + c) * 128 + of;
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2)
-                            *reinterpret_cast<uint4 *>(p.o + out_row * D + 4 * (c + e)) =
-                                make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
-                                           pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
-                                           pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
+                                for (int e = 0; e < 4; ++e) {
+                                    const float4 v = __ldcg(src + e * 128);
+                                    sum[e].x = fmaf(f, v.x, sum[e].x), sum[e].y = fmaf(f, v.y, sum[e].y);
+                                    sum[e].z = fmaf(f, v.z, sum[e].z), sum[e].w = fmaf(f, v.w, sum[e].w);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2)
+                                *reinterpret_cast<uint4 *>(p.o + to_row * D + out0 + 4 * (c + e)) =
+                                    make_uint4(pack_bf16(sum[e].x * one, sum[e].y * one), pack_bf16(sum[e].z * one, sum[e].w * one),
+                                               pack_bf16(sum[e + 1].x * one, sum[e + 1].y * one),
+                                               pack_bf16(sum[e + 1].z * one, sum[e + 1].w * one));
+                        }
+                        if (p.lse && out0 == 0 && row >> shift == 0) p.lse[to_row] = log_sum(M, L);
                     }
-                    if (p.lse && out0 == 0) p.lse[out_row] = log_sum(M, L);
                 }
                 named_sync(bar_id, bar_count);  // the ticket may be written again
             }
