@@ -21,7 +21,7 @@
 // sixteen rows of an mma.m16n8k16 and queries as its eight columns: a decode
 // step has h_q / h_kv query rows for a key/value head, four or eight as a rule,
 // and eight columns waste half as much as sixteen rows, in products and in
-// registers for O.  The rows of a (sequence, key/value head), at most 16 at a
+// registers for O.  The rows of a (sequence, key/value head), 8 or 16 at a
 // time, are a unit of ceil(tokens / 64) blocks.  All units lie on one line, and
 // CTA c takes its c-th equal part, so unequal lengths are balanced to a block.  A
 // unit that lies in several parts is joined by whichever CTA finishes last, from
@@ -52,7 +52,8 @@ constexpr int kUnitStart = 512;
 
 // Consumer warps by what a lane has to hold: D / 4 sums for every eight queries, D / 8 bytes of values, fragments.
 template <int D, int NT> struct RowsShape {
-    static constexpr int kWarps = D * NT <= 128 ? 16 : D * NT <= 256 ? 12 : 8;
+    static constexpr int kWarps = D * NT <= 128 ? 16 : 12;
+    static_assert(D * NT <= 256, "what a lane has room for");
     static constexpr int kGroups = kWarps / 4;
     static constexpr int kConsumers = 32 * kWarps, kThreads = kConsumers + 128;
     // What a thread has at launch, and the split between the loads' warpgroup and the others.
@@ -615,14 +616,12 @@ template <int D, int NT> cudaError_t launch(const CUtensorMap &k, const CUtensor
     return cudaGetLastError();
 }
 
-template <int NT> cudaError_t pick(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int d, cudaStream_t st) {
-    return d == 64 ? launch<64, NT>(k, v, p, st) : d == 128 ? launch<128, NT>(k, v, p, st) : launch<256, NT>(k, v, p, st);
-}
-
 }  // namespace
 
 cudaError_t attend_rows(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int d, cudaStream_t st) {
-    return (long long)p.max_len * p.group <= 8 ? pick<1>(k, v, p, d, st) : pick<2>(k, v, p, d, st);
+    if (d == 256) return launch<256, 1>(k, v, p, st);
+    if ((long long)p.max_len * p.group <= 8) return d == 64 ? launch<64, 1>(k, v, p, st) : launch<128, 1>(k, v, p, st);
+    return d == 64 ? launch<64, 2>(k, v, p, st) : launch<128, 2>(k, v, p, st);
 }
 
 }  // namespace paged
