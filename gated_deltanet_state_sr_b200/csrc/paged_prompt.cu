@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kSplit = NQ == 1;  // both softmax groups work on the one query tile
     extern __shared__ __align__(1024) uint8_t smem[];
     typename S::Misc &misc = *reinterpret_cast<typename S::Misc *>(smem + S::off_misc);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t base = tc::smem_u32(smem);
 
     if (threadIdx.x == 0) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = misc.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc.tmem, 0);
     Segment seg;
     bool alive = true;  // a wait that ran out ends a role; the others' waits then run out too
     auto wait = [&](uint64_t &bar, int phase) {
@@ -200,59 +200,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
-        if (warp == 12 && lane == 0) {
-            // ---- products
-            int kt = 0, vt = 0, w = 0;  // tiles of keys, stages of values, items (tile, query tile) so far
+        if (warp == 12) {
+            // ---- products, by one lane; the warp walks along so that addresses stay in uniform registers: 80 cycles an
+            // instruction otherwise, longer than most take to execute
+            auto ready = [&](uint64_t &bar, int phase) { return alive = __all_sync(0xffffffffu, wait(bar, phase)); };
+            int ks = 0, kp = 0, vs = 0, vp = 0, w = 0;  // the rings' stages and rounds; items (tile, query tile) so far
             for (int unit = 0; alive && line.next(seg); ++unit) {
-                const int tiles = seg.b1 - seg.b0;
-                if (!wait(misc.q_full, unit)) break;
-                const int items = tiles * NQ;
-                auto scores = [&](int i) {  // item i of the unit: buffer (w + i) & 1
-                    const int tile = i / NQ, j = i - tile * NQ, st = (kt + tile) % S::kKStages;
-                    if (!wait(misc.k_full[st], (kt + tile) / S::kKStages)) return false;
-                    tc::tc_fence_after();
-                    const uint32_t d = tmem + ((w + i) & 1) * 128;
-                    uint32_t on = 0;
-#pragma unroll 1
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int s = 0; s < D / 32; ++s) {
-                            const uint32_t at = (s * 32 / S::kSub) * 128 * S::kSub + (s * 32) % S::kSub;
-                            tc::mma_f8_ss(d, desc_k<D>(base + (j * 2 + part) * S::kQ + at),
-                                          desc_k<D>(base + S::off_k + st * S::kK + at), kIdescS, on);
-                            on = 1;
-                        }
-                    tc::mma_commit(&misc.s_full[(w + i) & 1]);
-                    if (j == NQ - 1) tc::mma_commit(&misc.k_empty[st]);
-                    return true;
-                };
+                if (!ready(misc.q_full, unit)) break;
+                const int items = __shfl_sync(0xffffffffu, (seg.b1 - seg.b0) * NQ, 0);
                 // S of two items ahead of P V of one
 #pragma unroll 1
                 for (int i = 0; i < items + 2; ++i) {
+                    const int j = NQ == 2 ? i & 1 : 0, b = (w + i) & 1;  // query tile; buffer of the scores
                     if (i >= 2) {
-                        const int tile = (i - 2) / NQ, j = (i - 2) - tile * NQ, b = (w + i) & 1;
-                        if (i == 2 && unit && !wait(misc.o_free, unit - 1)) break;
-                        if (!wait(misc.p_full[b], (w + i - 2) >> 1)) break;
+                        if (i == 2 && unit && !ready(misc.o_free, unit - 1)) break;
+                        if (!ready(misc.p_full[b], (w + i - 2) >> 1)) break;
+                        int st = vs, round = vp;
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
-                            const int n = vt + tile * 2 + h, st = n % S::kVStages;
-                            if (!wait(misc.v_full[st], n / S::kVStages)) break;
+                            if (!ready(misc.v_full[st], round)) break;
                             tc::tc_fence_after();
+                            if (tc::elect_one()) {
 #pragma unroll
-                            for (int s = 0; s < kHalf / 16; ++s)
-                                mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * (kSplit ? 64 : 32) + s * 8,
-                                           tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
-                                           idesc_pv<D>(), tile | h | s ? 1u : 0u);
-                            if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
+                                for (int s = 0; s < kHalf / 16; ++s)
+                                    mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * (kSplit ? 64 : 32) + s * 8,
+                                               tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
+                                               idesc_pv<D>(), i >= 2 + NQ || h || s ? 1u : 0u);
+                                if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
+                                if (h == 1) tc::mma_commit(&misc.pv_done[b]);
+                            }
+                            __syncwarp();
+                            if (++st == S::kVStages) st = 0, ++round;
                         }
                         if (!alive) break;
-                        tc::mma_commit(&misc.pv_done[b]);
+                        if (j == NQ - 1) vs = st, vp = round;
                     }
-                    if (i < items && !scores(i)) break;
+                    if (i < items) {
+                        if (!ready(misc.k_full[ks], kp)) break;
+                        tc::tc_fence_after();
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int s = 0; s < D / 32; ++s) {
+                                    const uint32_t at = (s * 32 / S::kSub) * 128 * S::kSub + (s * 32) % S::kSub;
+                                    tc::mma_f8_ss(tmem + b * 128, desc_k<D>(base + (j * 2 + part) * S::kQ + at),
+                                                  desc_k<D>(base + S::off_k + ks * S::kK + at), kIdescS, part || s ? 1u : 0u);
+                                }
+                            tc::mma_commit(&misc.s_full[b]);
+                            if (j == NQ - 1) tc::mma_commit(&misc.k_empty[ks]);
+                        }
+                        __syncwarp();
+                        if (j == NQ - 1 && ++ks == S::kKStages) ks = 0, ++kp;
+                    }
                 }
                 // a unit without tiles keeps the count of the sums' releases
-                if (items == 0 && unit && !wait(misc.o_free, unit - 1)) break;
-                kt += tiles, vt += 2 * tiles, w += items;
+                if (items == 0 && unit && !ready(misc.o_free, unit - 1)) break;
+                w += items;
             }
         } else if (warp == 13 || warp == 14) {
             // ---- loads: keys, and values by a warp of their own (a wait for either ring would hold up the other).  A
