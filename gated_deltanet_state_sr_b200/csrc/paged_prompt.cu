@@ -15,10 +15,10 @@
 //               shared memory.  e4m3 weights would do for neither accuracy nor
 //               range: many small weights beside a large one add up.
 // A CTA walks its part of the line of blocks (paged_attention.cuh).  Its warps:
-//   two groups of four: softmax, a row per thread, for two tiles of query rows
-//     (head dimension 256: one tile, whose scores have two buffers; the groups
-//     take half of a tile's columns each and exchange the rows' largest), and the
-//     queries' split at the start of a unit;
+//   four groups of four: softmax for two tiles of query rows (head dimension 256:
+//     two groups for one tile, whose scores have two buffers), and the queries'
+//     split at the start of a unit.  Two groups share a tile: a thread takes half
+//     of a row's columns, and the two of a row exchange its largest score;
 //   one group of four: values to half precision;
 //   a warp that issues the products, S of two items ahead of P V of one;
 //   a warp that loads pages of keys, and one for values.
@@ -39,32 +39,33 @@ namespace sr {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kTok = 128;       // cached tokens per tile
 constexpr int kHalf = 64;       // tokens per stage of values
 constexpr int kMinBlocks = 2;   // least tiles worth a CTA of their own
 constexpr int kUnitStart = 512; // what a unit costs beside its tiles, in tokens: the prompts above 280 us with 256 or
                                 // 768, 262 with 512 (at that stage of the kernel)
-// 256 x 160 + 128 x 96 + 128 x 96 = 512 x 128, what the block is launched with.
-constexpr int kSoftmaxRegs = 160, kConvertRegs = 96, kIssueRegs = 96;
-static_assert(256 * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= 512 * 128, "the split draws on the launch's");
 constexpr int kPoisonSlots = 8;  // units with tiles that the values may be ahead of the sums: fewer, by their ring
 
 template <int D> struct PromptSmem {
     static constexpr int kTiles = D == 256 ? 1 : 2;            // query tiles
     static constexpr int kRows = 128 * kTiles;
+    static constexpr int kSoftmax = 256 * kTiles, kThreads = kSoftmax + 256;
+    // of each role; the split draws on what the block is launched with
+    static constexpr int kLaunchRegs = kTiles == 1 ? 128 : 80;
+    static constexpr int kSoftmaxRegs = kTiles == 1 ? 160 : 96, kConvertRegs = kTiles == 1 ? 96 : 48, kIssueRegs = kTiles == 1 ? 96 : 48;
+    static_assert(kSoftmax * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs, "");
     static constexpr int kSub = D == 64 ? 64 : 128;            // bytes of an 8-bit row in shared memory
     static constexpr int kSubs = D == 256 ? 2 : 1;
     static constexpr int kQ = 128 * D;                         // one part of one query tile
     static constexpr int kK = kTok * D, kKStages = D == 256 ? 2 : 3;
     static constexpr int kRaw = kHalf * D, kRawStages = D == 256 ? 2 : 3;
-    static constexpr int kV = kHalf * D * 2, kVStages = D == 256 ? 2 : 4;
+    static constexpr int kV = kHalf * D * 2, kVStages = D == 256 ? 2 : 3;
     static constexpr int off_k = kTiles * 2 * kQ;
     static constexpr int off_raw = off_k + kKStages * kK;
     static constexpr int off_v = off_raw + kRawStages * kRaw;
-    // 32 output columns of every row, padded, for each softmax warp: of their own, or, at head dimension 256, in the
-    // queries' place once no product reads them
-    static constexpr int kPitch = 80, kStaging = D == 256 ? 0 : 8 * 32 * kPitch;
+    // 32 output columns of every row for each softmax warp: of their own, or, at head dimension 256, in the queries'
+    // place once no product reads them
+    static constexpr int kPitch = 64, kStaging = D == 256 ? 0 : 16 * 32 * kPitch;
     static constexpr int off_staging = D == 256 ? 0 : off_v + kVStages * kV;
     static constexpr int off_misc = off_v + kVStages * kV + kStaging;
     struct Misc {
@@ -75,7 +76,7 @@ template <int D> struct PromptSmem {
         uint64_t s_full[2], p_full[2], pv_done[2];
         union {
             LinePlace place;            // at the start
-            float top[2][2][128];       // where two threads share a row: what they exchange
+            float top[kTiles][2][2][128];  // what the two threads of a row exchange
         };
         uint32_t tmem;
         int poison[kPoisonSlots];
@@ -157,30 +158,30 @@ __device__ __forceinline__ uint32_t nan_columns(const AttnParams &p, const Segme
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ AttnParams p) {
     using S = PromptSmem<D>;
     constexpr int NQ = S::kTiles;
-    constexpr bool kSplit = NQ == 1;  // both softmax groups work on the one query tile
+    constexpr int kIssueWarp = S::kThreads / 32 - 4;
     extern __shared__ __align__(1024) uint8_t smem[];
     typename S::Misc &misc = *reinterpret_cast<typename S::Misc *>(smem + S::off_misc);
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t base = tc::smem_u32(smem);
 
     if (threadIdx.x == 0) {
-        tc::mbar_init(&misc.q_full, 256);
-        tc::mbar_init(&misc.o_free, 256);
+        tc::mbar_init(&misc.q_full, S::kSoftmax);
+        tc::mbar_init(&misc.o_free, S::kSoftmax);
         for (int i = 0; i < S::kKStages; ++i) tc::mbar_init(&misc.k_full[i], 1), tc::mbar_init(&misc.k_empty[i], 1);
         for (int i = 0; i < S::kRawStages; ++i) tc::mbar_init(&misc.raw_full[i], 1), tc::mbar_init(&misc.raw_empty[i], 128);
         for (int i = 0; i < S::kVStages; ++i) tc::mbar_init(&misc.v_full[i], 128), tc::mbar_init(&misc.v_empty[i], 1);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&misc.s_full[i], 1), tc::mbar_init(&misc.p_full[i], kSplit ? 256 : 128), tc::mbar_init(&misc.pv_done[i], 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&misc.s_full[i], 1), tc::mbar_init(&misc.p_full[i], 256), tc::mbar_init(&misc.pv_done[i], 1);
         for (int i = 0; i < kPoisonSlots; ++i) misc.poison[i] = 0;
         tc::fence_mbar_init();
     }
     Line<S::kRows, kTok, kUnitStart> line;
-    if (!line.template start<kThreads>(p, (long long)kMinBlocks * kTok * p.group, misc.place)) return;
-    if (warp == 12) {
+    if (!line.template start<S::kThreads>(p, (long long)kMinBlocks * kTok * p.group, misc.place)) return;
+    if (warp == kIssueWarp) {
         tc::tmem_alloc(&misc.tmem, 512);
         tc::tmem_relinquish();
     }
@@ -198,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return alive;
     };
 
-    if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
-        if (warp == 12) {
+    if (warp >= kIssueWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(S::kIssueRegs));
+        if (warp == kIssueWarp) {
             // ---- products, by one lane; the warp walks along so that addresses stay in uniform registers: 80 cycles an
             // instruction otherwise, longer than most take to execute
             auto ready = [&](uint64_t &bar, int phase) { return alive = __all_sync(0xffffffffu, wait(bar, phase)); };
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (tc::elect_one()) {
 #pragma unroll
                                 for (int s = 0; s < kHalf / 16; ++s)
-                                    mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * (kSplit ? 64 : 32) + s * 8,
+                                    mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * 64 + s * 8,
                                                tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
                                                idesc_pv<D>(), i >= 2 + NQ || h || s ? 1u : 0u);
                                 if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
@@ -258,10 +259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (items == 0 && unit && !ready(misc.o_free, unit - 1)) break;
                 w += items;
             }
-        } else if (warp == 13 || warp == 14) {
+        } else if (warp == kIssueWarp + 1 || warp == kIssueWarp + 2) {
             // ---- loads: keys, and values by a warp of their own (a wait for either ring would hold up the other).  A
             // page (64 rows of it at most) per lane; pages behind the sequence's end are not read.
-            const bool keys = warp == 13;
+            const bool keys = warp == kIssueWarp + 1;
             const CUtensorMap *map = keys ? &kmap : &vmap;
             uint64_t *full = keys ? misc.k_full : misc.raw_full, *empty = keys ? misc.k_empty : misc.raw_empty;
             const int tokens = keys ? kTok : kHalf, stages = keys ? S::kKStages : S::kRawStages;
@@ -287,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++st == stages) st = 0, ++round;
                 }
         }
-    } else if (warp >= 8) {
+    } else if (warp >= S::kSoftmax / 32) {
         // ---- values to half precision: token rows of 64 columns, 128-byte swizzle, the layout of an MN-major operand
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kConvertRegs));
-        const int t = threadIdx.x - 256;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(S::kConvertRegs));
+        const int t = threadIdx.x - S::kSoftmax;
         int vt = 0, filled = 0;  // filled: units with tiles so far
         while (alive && line.next(seg)) {
             const int unit = filled;
@@ -354,13 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ---- softmax: a query row per thread; at head dimension 256 two threads, each half of a tile's columns and of O's
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-        constexpr int kCols = kSplit ? kTok / 2 : kTok, kOut = kSplit ? D / 2 : D, kChunks = kCols / 32;
-        const int group = warp >> 2, q_tile = kSplit ? 0 : group;
+        // ---- softmax: a query row for two threads, each half of a tile's columns and of O's
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(S::kSoftmaxRegs));
+        constexpr int kCols = kTok / 2, kOut = D / 2, kChunks = kCols / 32;
+        const int q_tile = warp >> 3, group = warp >> 2 & 1;
         const int row = threadIdx.x & 127;
-        const int col0 = kSplit ? group * kCols : 0, out0 = kSplit ? group * kOut : 0;
-        const int bar_id = kSplit ? 1 : 1 + group, bar_count = kSplit ? 256 : 128;
+        const int col0 = group * kCols, out0 = group * kOut;
+        const int bar_id = 1 + q_tile;  // of the tile's 256 threads
+        // Exchanged: the largest scores of a tile, and a unit's sums.  Two query tiles: a place for each, since the next
+        // tile's scores come after all have read.  One: the buffers' in turn.
+        float(*top_of)[2][128] = misc.top[q_tile];
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t o_at = tmem + lanes + 256 + q_tile * 128 + out0;
         int w = 0, filled = 0;  // items of the CTA, units with tiles so far
@@ -369,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows of the query tile that this warp splits into hi + lo, D / 8 lanes a row, 16 bytes each.  The bytes come
         // asynchronously, four elements to where their hi will lie and four to where their lo will, for all rows at
         // once, and, where the tile's place is free by then, while the unit before ends.
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = kSplit ? 16 : 32;
-        const int sub = lane / kLanes, c8 = lane % kLanes, row0 = kSplit ? warp * 16 : (warp & 3) * 32;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kMine = 16;
+        const int sub = lane / kLanes, c8 = lane % kLanes, row0 = (warp & 7) * 16;
         const uint32_t hi_at = base + q_tile * 2 * S::kQ, lo_at = hi_at + S::kQ;
         // token and head of row x of a tile, from its first row's
         auto place = [&](const Segment &sg, int token0, int head0, int x, int &token, int &h) {
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_async_smem();
             tc::mbar_arrive(&misc.q_full);
-            if (kSplit) named_sync(bar_id, bar_count); else __syncwarp();
+            named_sync(bar_id, 256);
             return scales[row];
         };
         // Of a unit: what is left to do once its products are issued, while the next unit's begin.
@@ -437,12 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool real = false;
         float m = kNone, l = 0.f, row_scale = 0.f;
         auto finish = [&]() {
-            if (kSplit) {  // both halves' sums, in the buffer that the last tile did not use
-                float(*sums)[128] = misc.top[(last + 1) & 1];
-                sums[group][row] = l;
-                named_sync(bar_id, bar_count);
-                l = sums[0][row] + sums[1][row];
-            }
+            float(*sums)[128] = top_of[NQ == 1 ? (last + 1) & 1 : 1];
+            sums[group][row] = l;
+            named_sync(bar_id, 256);
+            l = sums[0][row] + sums[1][row];
             if (tiles > 0 && !wait(misc.pv_done[last & 1], last >> 1)) return;
             tc::tc_fence_after();
 
@@ -480,18 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 32; ++e) y[e] = hit >> e & 1 ? 0x7fc00000u : y[e];
                 }
                 if (seg.whole) {
+                    // chunk c of row r lies at c ^ (r / 2 % 4): neither the rows nor the chunks of eight lanes meet in a bank
                     const uint32_t mine = tc::smem_u32(staging) + lane * S::kPitch;
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        sts128(mine + e * 2, pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
+                        sts128(mine + ((e / 8 ^ (lane >> 1 & 3)) << 4), pack_bf16(__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv),
                                pack_bf16(__uint_as_float(y[e + 2]) * inv, __uint_as_float(y[e + 3]) * inv),
                                pack_bf16(__uint_as_float(y[e + 4]) * inv, __uint_as_float(y[e + 5]) * inv),
                                pack_bf16(__uint_as_float(y[e + 6]) * inv, __uint_as_float(y[e + 7]) * inv));
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (lane & 3) * 16);
+                        const uint4 v = lds128(tc::smem_u32(staging) + ((lane >> 2) + 8 * i) * S::kPitch + (((lane ^ lane >> 3) & 3) << 4));
                         if (to[i] >= 0) *reinterpret_cast<uint4 *>(p.o + to[i] + c) = v;
                     }
                 } else if (real) {
@@ -507,14 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (real && !bad_pages && p.lse && out0 == 0) p.lse[out_row] = log_sum(m, l);
             } else {
                 if (out0 == 0) p.part_ml[(slot * NQ + q_tile) * 128 + row] = make_float2(m, l);
-                named_sync(bar_id, bar_count);
+                named_sync(bar_id, 256);
                 if (row == 0 && out0 == 0) {
                     int *ticket = &p.tickets[first_cta * NQ + q_tile];
                     const bool mine = take_ticket(ticket) == last_cta - first_cta;
                     if (mine) *ticket = 0;
                     misc.ticket[q_tile] = mine;
                 }
-                named_sync(bar_id, bar_count);
+                named_sync(bar_id, 256);
                 const int mine = min(128, seg.rows - q_tile * 128);  // rows of the tile that there are
                 if (misc.ticket[q_tile] && mine > 0 && !bad_pages) {
                     const int parts = last_cta - first_cta + 1;
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (p.lse && out0 == 0 && row >> shift == 0) p.lse[to_row] = log_sum(M, L);
                     }
                 }
-                named_sync(bar_id, bar_count);  // the ticket may be written again
+                named_sync(bar_id, 256);  // the ticket may be written again
             }
         };
         Segment next;
@@ -566,19 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (alive) {
             // Every product with the last unit's queries is done.  The next one's come first, so that its scores are
             // formed while the last one's sums are written; where those go out by way of the queries' place, after them.
-            if (kSplit && have) {
+            if (NQ == 1 && have) {
                 finish();
-                named_sync(bar_id, bar_count);
+                named_sync(bar_id, 256);
                 more = line.next(next);
             }
             if (more) {
                 fetch_queries(next);
                 row_scale = split_queries();
             }
-            if (!kSplit && have) finish();
+            if (NQ == 2 && have) finish();
             if (!more || !alive) break;
             seg = next;
-            if (!kSplit) more = line.next(next);
+            if (NQ == 2) more = line.next(next);
             have = true;
             tiles = seg.b1 - seg.b0;
             const int g0 = seg.tile * S::kRows, token0 = g0 / p.group, head0 = g0 - token0 * p.group;
@@ -590,16 +593,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool bad = false;
                 const int pages = (seg.kv + p.page - 1) >> p.page_shift;
 #pragma unroll 1
-                for (int i = kSplit ? threadIdx.x : row; i < pages; i += bar_count) {
+                for (int i = threadIdx.x & 255; i < pages; i += 256) {
                     const int page = p.table[(long long)seg.seq * p.max_pages + i];
                     bad |= page < 0 || page >= p.n_pages;
                 }
-                bad_pages = named_or(bar_id, bar_count, bad);
+                bad_pages = named_or(bar_id, 256, bad);
                 if (bad_pages && threadIdx.x == 0) atomicOr(p.status, SR_DEV_BAD_INDEX);
                 checked = seg.seq;
             }
             m = kNone, l = 0.f;
-            // Lane g of every eight (four) holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
+            // Lane g of every four holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
             // columns, loaded a tile ahead, their page two.
             auto page_of = [&](int b) {
                 const int at = b * kTok + col0 + (lane & (kCols / 16 - 1)) * 16;
@@ -648,11 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (edge) tc::tmem_st_wait();
-                if (kSplit) {  // the other half's largest
-                    misc.top[buf][group][row] = top;
-                    named_sync(bar_id, bar_count);
-                    top = fmaxf(misc.top[buf][0][row], misc.top[buf][1][row]);
-                }
+                float(*tops)[128] = top_of[NQ == 1 ? buf : 0];  // with the other half's
+                tops[group][row] = top;
+                named_sync(bar_id, 256);
+                top = fmaxf(tops[0][row], tops[1][row]);
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     const float next = fmaxf(m, top), f = exp2f(m - next);
                     m = next, l *= f;
@@ -708,14 +710,14 @@ done:
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == 12) tc::tmem_dealloc(tmem, 512);
+    if (warp == kIssueWarp) tc::tmem_dealloc(tmem, 512);
 }
 
 template <int D> cudaError_t launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t st) {
     const int bytes = PromptSmem<D>::bytes;
     cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    prompt_kernel<D><<<kPromptCtas, kThreads, bytes, st>>>(k, v, p);
+    prompt_kernel<D><<<kPromptCtas, PromptSmem<D>::kThreads, bytes, st>>>(k, v, p);
     return cudaGetLastError();
 }
 
