@@ -602,21 +602,23 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                 checked = seg.seq;
             }
             m = kNone, l = 0.f;
-            // Lane g of every four holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's
-            // columns, loaded a tile ahead, their page two.
+            // Lane g of every four holds the scales of the tile's tokens 16 g .. 16 g + 15 of this thread's columns (of the
+            // sequence's last page behind its end), loaded a tile ahead, their page two.  What was loaded is looked at a
+            // tile later, without a branch on the way, so that no load is waited for.
             auto page_of = [&](int b) {
-                const int at = b * kTok + col0 + (lane & (kCols / 16 - 1)) * 16;
-                return b < seg.b1 && at < seg.kv ? page_at(p, seg.seq, at) : -1;
+                const int at = min(b * kTok + col0 + (lane & (kCols / 16 - 1)) * 16, seg.kv - 1);
+                return p.table[(long long)seg.seq * p.max_pages + (at >> p.page_shift)];
             };
             float ks_next = 1.f, vs_next = 1.f;
             auto load_scales = [&](int page) {
-                if (page >= 0) {
-                    const long long block = (long long)page * p.h_kv + seg.head;
-                    ks_next = p.k_scale[block], vs_next = p.v_scale[block];
-                }
+                const long long block = (long long)(page < 0 || page >= p.n_pages ? 0 : page) * p.h_kv + seg.head;
+                ks_next = p.k_scale[block], vs_next = p.v_scale[block];
             };
-            load_scales(page_of(seg.b0));
-            int page_next = page_of(seg.b0 + 1);
+            int page_next = 0;
+            if (tiles > 0) {
+                load_scales(page_of(seg.b0));
+                page_next = page_of(seg.b0 + 1);
+            }
             for (int t = 0; t < tiles; ++t) {
                 const int item = w + t * NQ + q_tile, buf = item & 1;
                 const int tok0 = (seg.b0 + t) * kTok + col0;
