@@ -221,11 +221,12 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             if (!ready(misc.v_full[st], round)) break;
                             tc::tc_fence_after();
+                            const uint64_t values = tc::sdesc_sw128(base + S::off_v + st * S::kV, kHalf * 128, 1024);
                             if (tc::elect_one()) {
 #pragma unroll
                                 for (int s = 0; s < kHalf / 16; ++s)
                                     mma_f16_ts(tmem + 256 + j * 128, tmem + b * 128 + h * 64 + s * 8,
-                                               tc::sdesc_sw128(base + S::off_v + st * S::kV + s * 2048, kHalf * 128, 1024),
+                                               values + s * (2048 >> 4),
                                                idesc_pv<D>(), i >= 2 + NQ || h || s ? 1u : 0u);
                                 if (j == NQ - 1) tc::mma_commit(&misc.v_empty[st]);
                                 if (h == 1) tc::mma_commit(&misc.pv_done[b]);
@@ -239,14 +240,19 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                     if (i < items) {
                         if (!ready(misc.k_full[ks], kp)) break;
                         tc::tc_fence_after();
+                        // sums of descriptors: 2 % sooner at head dimensions of 64 and 128, 3 % later at 256
+                        const uint64_t queries = desc_k<D>(base + j * 2 * S::kQ), keys = desc_k<D>(base + S::off_k + ks * S::kK);
                         if (tc::elect_one()) {
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
                                 for (int s = 0; s < D / 32; ++s) {
                                     const uint32_t at = (s * 32 / S::kSub) * 128 * S::kSub + (s * 32) % S::kSub;
-                                    tc::mma_f8_ss(tmem + b * 128, desc_k<D>(base + (j * 2 + part) * S::kQ + at),
-                                                  desc_k<D>(base + S::off_k + ks * S::kK + at), kIdescS, part || s ? 1u : 0u);
+                                    if (NQ == 2)
+                                        tc::mma_f8_ss(tmem + b * 128, queries + ((part * S::kQ + at) >> 4), keys + (at >> 4), kIdescS, part || s);
+                                    else
+                                        tc::mma_f8_ss(tmem + b * 128, desc_k<D>(base + part * S::kQ + at),
+                                                      desc_k<D>(base + S::off_k + ks * S::kK + at), kIdescS, part || s);
                                 }
                             tc::mma_commit(&misc.s_full[b]);
                             if (j == NQ - 1) tc::mma_commit(&misc.k_empty[ks]);
@@ -361,7 +367,8 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
         const int q_tile = warp >> 3, group = warp >> 2 & 1;
         const int row = threadIdx.x & 127;
         const int col0 = group * kCols, out0 = group * kOut;
-        const int bar_id = 1 + q_tile;  // of the tile's 256 threads
+        const int bar_id = 1 + q_tile;  // of the tile's 256 threads,
+        const int row_bar = 3 + q_tile * 4 + (warp & 3);  // and of the 64 whose rows are the same
         // Exchanged: the largest scores of a tile, and a unit's sums.  Two query tiles: a place for each, since the next
         // tile's scores come after all have read.  One: the buffers' in turn.
         float(*top_of)[2][128] = misc.top[q_tile];
@@ -443,7 +450,7 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
         auto finish = [&]() {
             float(*sums)[128] = top_of[NQ == 1 ? (last + 1) & 1 : 1];
             sums[group][row] = l;
-            named_sync(bar_id, 256);
+            named_sync(row_bar, 64);
             l = sums[0][row] + sums[1][row];
             if (tiles > 0 && !wait(misc.pv_done[last & 1], last >> 1)) return;
             tc::tc_fence_after();
@@ -630,32 +637,42 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                 const uint32_t s_at = tmem + lanes + buf * 128 + col0;
                 if (!wait(misc.s_full[buf], item >> 1)) break;
                 tc::tc_fence_after();
-                // Two passes over the scores, 32 at a time, so that registers hold no row of 128 and the loops stay in the
-                // instruction cache: the largest of every 16 (whose scales are alike), then the weights.
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int q = 0; q < kChunks; ++q) {
-                    uint32_t y[32];
-                    tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
+                // Two passes over the scores, 32 at a time: the largest of every 16 (whose scales are alike), then the
+                // weights.  Between them registers hold the scores where there are enough; elsewhere they are loaded again.
+                constexpr bool kKeep = NQ == 1;
+                constexpr int kUnroll = kKeep ? kChunks : 1;
+                uint32_t y[kKeep ? kChunks : 1][32];
+                if (kKeep) {
+#pragma unroll
+                    for (int q = 0; q < kChunks; ++q) tc::tmem_ld_32x32b_x32(s_at + 32 * q, y[kKeep ? q : 0]);
                     tc::tmem_ld_wait();
+                }
+                float top = -INFINITY;
+#pragma unroll kUnroll
+                for (int q = 0; q < kChunks; ++q) {
+                    uint32_t(&x)[32] = y[kKeep ? q : 0];
+                    if (!kKeep) {
+                        tc::tmem_ld_32x32b_x32(s_at + 32 * q, x);
+                        tc::tmem_ld_wait();
+                    }
                     if (edge) {  // -inf where the row does not see, also for the second pass
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) y[c] = tok0 + 32 * q + c < seen ? y[c] : 0xff800000u;
-                        tc::tmem_st_32x32b_x32(s_at + 32 * q, y);
+                        for (int c = 0; c < 32; ++c) x[c] = tok0 + 32 * q + c < seen ? x[c] : 0xff800000u;
+                        if (!kKeep) tc::tmem_st_32x32b_x32(s_at + 32 * q, x);
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float most[2] = {__uint_as_float(y[16 * h]), __uint_as_float(y[16 * h + 1])};
+                        float most[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
 #pragma unroll
-                        for (int c = 2; c < 16; ++c) most[c & 1] = fmaxf(most[c & 1], __uint_as_float(y[16 * h + c]));
+                        for (int c = 2; c < 16; ++c) most[c & 1] = fmaxf(most[c & 1], __uint_as_float(x[16 * h + c]));
                         const float k = row_scale * __shfl_sync(0xffffffffu, ks, 2 * q + h);
                         top = fmaxf(top, fmaf(fmaxf(most[0], most[1]), k, __shfl_sync(0xffffffffu, lv, 2 * q + h)));
                     }
                 }
-                if (edge) tc::tmem_st_wait();
+                if (!kKeep && edge) tc::tmem_st_wait();
                 float(*tops)[128] = top_of[NQ == 1 ? buf : 0];  // with the other half's
                 tops[group][row] = top;
-                named_sync(bar_id, 256);
+                named_sync(row_bar, 64);
                 top = fmaxf(tops[0][row], tops[1][row]);
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     const float next = fmaxf(m, top), f = exp2f(m - next);
@@ -676,11 +693,13 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                 }
                 const float z = m - kShift;
                 // weights of columns 32 q .., over 16 columns of the scores' own, all of them read already
-#pragma unroll 1
+#pragma unroll kUnroll
                 for (int q = 0; q < kChunks; ++q) {
-                    uint32_t y[32], out[16];
-                    tc::tmem_ld_32x32b_x32(s_at + 32 * q, y);
-                    tc::tmem_ld_wait();
+                    uint32_t(&x)[32] = y[kKeep ? q : 0], out[16];
+                    if (!kKeep) {
+                        tc::tmem_ld_32x32b_x32(s_at + 32 * q, x);
+                        tc::tmem_ld_wait();
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float k = row_scale * __shfl_sync(0xffffffffu, ks, 2 * q + h);
@@ -688,8 +707,8 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
                         float sum[2] = {0.f, 0.f};
 #pragma unroll
                         for (int c = 16 * h; c < 16 * h + 16; c += 2) {
-                            const float a = ex2(fmaf(__uint_as_float(y[c]), k, v));
-                            const float b = ex2(fmaf(__uint_as_float(y[c + 1]), k, v));
+                            const float a = ex2(fmaf(__uint_as_float(x[c]), k, v));
+                            const float b = ex2(fmaf(__uint_as_float(x[c + 1]), k, v));
                             sum[0] += a, sum[1] += b;
                             out[c / 2] = pack_f16(a, b);
                         }
