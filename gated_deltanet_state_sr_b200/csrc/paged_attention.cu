@@ -9,11 +9,12 @@ namespace paged {
 namespace {
 
 // Few rows: reading the cache bounds the call, and the kernel that takes 8 or 16 rows at a time over it is sooner than
-// 128-row tiles are.  Measured (us, few and many): 16 requests over 8192 tokens, 8 heads of 128, 24 rows 134 and 217, 48
-// rows 192 and 219, 64 rows 247 and 215; 4 requests 24 rows 50 and 72.  At head dimension 256 sixteen rows leave a lane
-// no room: 16 requests over 4096, 4 heads, 16 rows 84 and 60, 8 rows 42 and 60.
+// 128-row tiles are.  Measured (us, few and many), heads of 128: 16 requests over 8192 tokens, 8 heads, 16 rows 79 and
+// 188, 32 rows 135 and 185, 48 rows 191 and 187; one request over 32768 32 rows 49 and 70; 64 requests over 512 tokens 16
+// rows 51 and 87, 32 rows 88 and 86, 48 rows 121 and 89.  At head dimension 256 sixteen rows leave a lane no room: 16
+// requests over 4096, 4 heads, 16 rows 84 and 60, 8 rows 42 and 60.
 bool few_rows(const sr_paged_attention_args *a) {
-    return (long long)a->max_seqlen * (a->h_q / a->h_kv) <= (a->head_dim == 256 ? 8 : 48);
+    return (long long)a->max_seqlen * (a->h_q / a->h_kv) <= (a->head_dim == 256 ? 8 : 32);
 }
 
 // Tickets, then the partial sums (two parts for every CTA) and their statistics.

@@ -26,13 +26,15 @@
 // times 128 columns, or 256).
 //
 // Measured: 1639 tokens behind 32768 cached (16 / 4 heads of 256, 0.90 TFLOP)
-// 837 us, 1.08 PFLOP/s: shared memory, which every product reads both operands
-// from and the values pass twice more, is busy for 2800 of a tile's 4000 cycles
-// and the products for 2050.  Eight prompts of 512 to 2048 tokens (32 / 8 heads
-// of 128, 0.10 TFLOP) 247 us: five tiles a unit on average, whose start and end
-// cost as much as three tiles, and the softmax's own latency.  The code is kept
-// small on purpose: at 165 KB of instructions the prompts took 512 us, at 113 KB
-// 344, the rest alike.
+// 690 to 710 us, 1.3 PFLOP/s, the rate that the power cap leaves a plain product.
+// Eight prompts of 512 to 2048 tokens (32 / 8 heads of 128, 0.10 TFLOP) 207 us:
+// five tiles a unit on average, whose start and end cost as much as four tiles.
+// 2048 tokens behind 32768, 32 / 8 heads of 128, 1034 us: a tile of 2 x 128 rows
+// takes 4300 cycles, the products 2050 of them; the scores of a row's next tile
+// wait for the product with its weights (tensor memory holds no third buffer), so
+// that a product, two passes over the scores and a product follow one another.
+// The code is kept small on purpose: at 165 KB of instructions the prompts took
+// 512 us, at 113 KB 344, the rest alike.
 #include "paged_attention.cuh"
 
 namespace sr {
@@ -42,18 +44,20 @@ namespace {
 constexpr int kTok = 128;       // cached tokens per tile
 constexpr int kHalf = 64;       // tokens per stage of values
 constexpr int kMinBlocks = 2;   // least tiles worth a CTA of their own
-constexpr int kUnitStart = 512; // what a unit costs beside its tiles, in tokens: the prompts above 280 us with 256 or
-                                // 768, 262 with 512 (at that stage of the kernel)
 constexpr int kPoisonSlots = 8;  // units with tiles that the values may be ahead of the sums: fewer, by their ring
 
 template <int D> struct PromptSmem {
     static constexpr int kTiles = D == 256 ? 1 : 2;            // query tiles
     static constexpr int kRows = 128 * kTiles;
+    // What a unit costs beside its tiles, in tokens.  Heads of 128, prompts of 512 to 2048: 222 us with 256 or 768, 207
+    // with 512; heads of 256, eight prompts of 2048: 412 with 512, 378 with 768, 366 with 1024, 380 with 1536.
+    static constexpr int kUnitStart = kTiles == 1 ? 1024 : 512;
     static constexpr int kSoftmax = 256 * kTiles, kThreads = kSoftmax + 256;
-    // of each role; the split draws on what the block is launched with
+    // Registers of each role.  The split draws on what the block is launched with, and would wait for ever if that were
+    // less (launch() looks).
     static constexpr int kLaunchRegs = kTiles == 1 ? 128 : 80;
     static constexpr int kSoftmaxRegs = kTiles == 1 ? 160 : 96, kConvertRegs = kTiles == 1 ? 96 : 48, kIssueRegs = kTiles == 1 ? 96 : 48;
-    static_assert(kSoftmax * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs, "");
+    static_assert(kSoftmax * kSoftmaxRegs + 128 * kConvertRegs + 128 * kIssueRegs <= kThreads * kLaunchRegs, "the split draws on the launch's");
     static constexpr int kSub = D == 64 ? 64 : 128;            // bytes of an 8-bit row in shared memory
     static constexpr int kSubs = D == 256 ? 2 : 1;
     static constexpr int kQ = 128 * D;                         // one part of one query tile
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
         for (int i = 0; i < kPoisonSlots; ++i) misc.poison[i] = 0;
         tc::fence_mbar_init();
     }
-    Line<S::kRows, kTok, kUnitStart> line;
+    Line<S::kRows, kTok, S::kUnitStart> line;
     if (!line.template start<S::kThreads>(p, (long long)kMinBlocks * kTok * p.group, misc.place)) return;
     if (warp == kIssueWarp) {
         tc::tmem_alloc(&misc.tmem, 512);
@@ -736,6 +740,11 @@ done:
 
 template <int D> cudaError_t launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t st) {
     const int bytes = PromptSmem<D>::bytes;
+    static const bool enough = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, prompt_kernel<D>) == cudaSuccess && a.numRegs >= PromptSmem<D>::kLaunchRegs;
+    }();
+    if (!enough) return cudaErrorLaunchOutOfResources;
     cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     prompt_kernel<D><<<kPromptCtas, PromptSmem<D>::kThreads, bytes, st>>>(k, v, p);

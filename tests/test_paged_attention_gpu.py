@@ -136,10 +136,11 @@ def test_long_caches_are_shared_and_joined(sr, d, page):
     check(sr, make([1, 2, 1], [9000, 100, 12345], 4, 1, d, page, seed=2))
 
 
-@pytest.mark.parametrize("d,h_q,h_kv,new", [(256, 8, 1, 1), (256, 9, 1, 1), (256, 4, 1, 2), (256, 4, 1, 3), (128, 8, 2, 12),
+@pytest.mark.parametrize("d,h_q,h_kv,new", [(256, 8, 1, 1), (256, 9, 1, 1), (256, 4, 1, 2), (256, 4, 1, 3), (128, 8, 2, 8),
+                                            (128, 8, 2, 9), (64, 32, 1, 1), (64, 33, 1, 1), (64, 4, 1, 8), (128, 8, 2, 12),
                                             (128, 8, 2, 13), (64, 48, 1, 1), (64, 49, 1, 1), (64, 6, 1, 8)], ids=str)
 def test_either_side_of_the_kernels_border(sr, d, h_q, h_kv, new):
-    """Eight query rows and more at head dimension 256, 48 and more below; several row tiles of the few-rows kernel."""
+    """Eight query rows and more at head dimension 256, 32 and more below; several row tiles of the few-rows kernel."""
     check(sr, make([new, 1, new], [new, 777, 130], h_q, h_kv, d, 32, seed=h_q + new))
 
 
