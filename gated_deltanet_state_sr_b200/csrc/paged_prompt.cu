@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(PromptSmem<D>::kThreads, 1)
     if (warp >= kIssueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(S::kIssueRegs));
         if (warp == kIssueWarp) {
-            // ---- products, by one lane; the warp walks along so that addresses stay in uniform registers: 80 cycles an
-            // instruction otherwise, longer than most take to execute
+            // ---- products, by one elected lane while the warp walks along.  With a lane alone in this branch they, their
+            // waits and their commits kept it busy for 6000 cycles a tile of 2 x 128 rows of 128, longer than all else;
+            // so 3600.
             auto ready = [&](uint64_t &bar, int phase) { return alive = __all_sync(0xffffffffu, wait(bar, phase)); };
             int ks = 0, kp = 0, vs = 0, vp = 0, w = 0;  // the rings' stages and rounds; items (tile, query tile) so far
             for (int unit = 0; alive && line.next(seg); ++unit) {
